@@ -236,6 +236,83 @@ SVG2_API int svg2_dense_attn_workspace_size(int B, int H, int N, int d, size_t* 
 SVG2_API int svg2_dense_attn(const void* Q, const void* K, const void* V, int B, int H, int N, int d, float scale,
                              void* O, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * Training: the attention calls above with the log-sum-exp that their gradients need, and the gradients.
+ * The pages train nothing; these let a model that uses the layer be fine-tuned through it.
+ *
+ * svg2_dense_attn_lse / svg2_sparse_attn_lse are svg2_dense_attn / svg2_sparse_attn (same arguments,
+ * workspace, errors and O, bit for bit) that also write
+ *   (scale must be > 0 and finite here and in the gradient calls: SVG2_ERR_INVALID_ARG otherwise)
+ *   lse      float [B,H,N], out: lse_i = log sum_j exp(scale * q_i.k_j) over the row's keys, indexed by
+ *            (permuted) row, whether perm_q is given or not; -inf for a row that keeps no key (O is 0). */
+SVG2_API int svg2_dense_attn_lse(const void* Q, const void* K, const void* V, int B, int H, int N, int d, float scale,
+                                 void* O, float* lse, void* ws, size_t ws_bytes, void* stream);
+SVG2_API int svg2_sparse_attn_lse(const void* Qp, const void* Kp, const void* Vp, const int32_t* q_off,
+                                  const int32_t* k_off, const int32_t* sel_count, const int32_t* sel_idx, int B,
+                                  int H, int N, int d, int nQ, int nK, float scale, const int32_t* perm_q, void* O,
+                                  float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of dense attention.  With P_ij = exp(scale * q_i.k_j - lse_i), recomputed tile by tile, and
+ * delta_i = dO_i.O_i:  dV = P^T dO,  dS = P o (dO V^T - delta),  dQ = scale dS K,  dK = scale dS^T Q.
+ *   Q, K, V, O, dO  bf16 [B,H,N,d] (d = 128 or 64), 16-byte aligned; O and lse as svg2_dense_attn_lse wrote them.
+ *   dQ, dK, dV      bf16 [B,H,N,d], out, 16-byte aligned; they may alias neither each other nor an input.
+ *   ws              at least svg2_dense_attn_bwd_workspace_size() bytes, 256-byte aligned (enough for
+ *                   svg2_dense_attn_lse too); holds the status word.
+ * P and dS are rounded to bf16 for the products, sums are float32; the results are the same on every run.
+ * Errors as svg2_dense_attn. */
+SVG2_API int svg2_dense_attn_bwd_workspace_size(int B, int H, int N, int d, size_t* bytes);
+SVG2_API int svg2_dense_attn_bwd(const void* Q, const void* K, const void* V, const void* O, const float* lse,
+                                 const void* dO, int B, int H, int N, int d, float scale, void* dQ, void* dK,
+                                 void* dV, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of the variable-block sparse attention for a fixed plan: the formulas above over the kept
+ * (query, key) pairs.  (The selection and the clustering have no gradient.)
+ *   Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, perm_q  as given to svg2_sparse_attn_lse; lse as it wrote it.
+ *            Each row's kept list must be in range and name a K cluster at most once (as svg2_select's
+ *            does); another one latches SVG2_ERR_DEVICE_BOUNDS and the gradients are not written.
+ *   O, dO    bf16 [B,H,N,d], by token if perm_q is given, else by permuted row.
+ *   dQ       bf16 [B,H,N,d], out: by token if perm_q is given, else by permuted row.
+ *   dK, dV   bf16 [B,H,N,d], out: by token if perm_k (optional int32 [B,H,N], token of each permuted K row) is
+ *            given, else by permuted row.  Rows that no kept pair holds get zeros; rows outside
+ *            every cluster are not written.
+ *   ws       at least svg2_sparse_attn_bwd_workspace_size() bytes (enough for svg2_sparse_attn_lse too).
+ * Errors as svg2_sparse_attn. */
+SVG2_API int svg2_sparse_attn_bwd_workspace_size(int B, int H, int N, int d, int nQ, int nK, size_t* bytes);
+SVG2_API int svg2_sparse_attn_bwd(const void* Qp, const void* Kp, const void* Vp, const void* O, const float* lse,
+                                  const void* dO, const int32_t* q_off, const int32_t* k_off,
+                                  const int32_t* sel_count, const int32_t* sel_idx, int B, int H, int N, int d,
+                                  int nQ, int nK, float scale, const int32_t* perm_q, const int32_t* perm_k,
+                                  void* dQ, void* dK, void* dV, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Layer norm over the last dimension, as models put in front of the attention's Q and K (width = d, rows =
+ * B*H*N) or of the layer's input:
+ *   mean = sum x / width, rstd = (sum (x - mean)^2 / width + eps)^(-1/2), y = (x - mean) rstd gamma + beta.
+ *   X      [rows, width] bf16 or f32 (dtype), aligned to its element.  Y  the same type, out (Y == X: in place).
+ *   gamma, beta  float [width], optional (NULL: 1 and 0).
+ *   mean, rstd   float [rows], out, optional: svg2_layer_norm_bwd reads them.
+ * 1 <= width <= SVG2_MAX_NORM_WIDTH, 1 <= rows < 2^31, eps >= 0 and finite.  Sums are float32.  One kernel on
+ * `stream`, no workspace.  Errors: SVG2_ERR_INVALID_ARG, SVG2_ERR_UNSUPPORTED (sizes), SVG2_ERR_CUDA. */
+#define SVG2_MAX_NORM_WIDTH 8192
+SVG2_API int svg2_layer_norm(const void* X, int dtype, const float* gamma, const float* beta, long long rows,
+                             int width, float eps, void* Y, float* mean, float* rstd, void* stream);
+
+/*
+ * Gradients of svg2_layer_norm: with xhat = (x - mean) rstd and g = dY gamma,
+ *   dX = rstd (g - sum g / width - xhat (sum g xhat) / width),  dgamma = sum_rows dY xhat,  dbeta = sum_rows dY.
+ *   X, dY  [rows, width] of one type (dtype); dX the same type, out (dX == dY or dX == X: in place).
+ *   gamma  float [width], optional (NULL: 1); mean, rstd  float [rows] as svg2_layer_norm wrote them.
+ *   dgamma, dbeta  float [width], out, optional.  Sums are float32, in a fixed order: the same on every run.
+ *   ws     at least svg2_layer_norm_bwd_workspace_size() bytes, 256-byte aligned (a zeroed status area, as in
+ *          every workspace, then the partial sums).
+ * Two kernels on `stream`.  Sizes and errors as svg2_layer_norm, and SVG2_ERR_WORKSPACE. */
+SVG2_API int svg2_layer_norm_bwd_workspace_size(long long rows, int width, size_t* bytes);
+SVG2_API int svg2_layer_norm_bwd(const void* X, const void* dY, int dtype, const float* gamma, const float* mean,
+                                 const float* rstd, long long rows, int width, void* dX, float* dgamma,
+                                 float* dbeta, void* ws, size_t ws_bytes, void* stream);
+
 /* Inverse permutation of output rows (Method (2)): O[b,h,perm[b,h,j],:] = Op[b,h,j,:], bf16. */
 SVG2_API int svg2_unpermute(const void* Op, const int32_t* perm, int B, int H, int N, int d, void* O, void* stream);
 

@@ -5,7 +5,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 
 #include "svg2.h"
@@ -34,6 +36,11 @@ EncodeTiledFn encode_fn() {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int to_status(cudaError_t e) { return e == cudaSuccess ? SVG2_OK : SVG2_ERR_CUDA; }
+
+bool finite_scale(float s) { return s == s && s != INFINITY && s != -INFINITY; }
+// The training calls: the softmax's maximum is taken before the scale, so a scale <= 0 would not be stable
+// (and would turn the -inf of masked columns into +inf or NaN).
+bool training_scale(float s) { return s > 0.f && s != INFINITY; }
 
 bool valid_dtype(int dt) { return dt == SVG2_BF16 || dt == SVG2_F32; }
 
@@ -386,28 +393,49 @@ int svg2_permute(const void* X, int dtype, const int32_t* labels, int B, int H, 
   }
 }
 
+static int sparse_attn_call(const void* Qp, const void* Kp, const void* Vp, const int32_t* q_off,
+                            const int32_t* k_off, const int32_t* sel_count, const int32_t* sel_idx, int B, int H,
+                            int N, int d, int nQ, int nK, float scale, const int32_t* perm_q, void* O, float* lse,
+                            void* ws, size_t ws_bytes, void* stream) {
+  int r = check_sizes(B, H, N, d);
+  if (r == SVG2_OK) r = check_k(nQ, N);
+  if (r == SVG2_OK) r = check_k(nK, N);
+  if (r != SVG2_OK) return r;
+  if (Qp == nullptr || Kp == nullptr || Vp == nullptr || q_off == nullptr || k_off == nullptr ||
+      sel_count == nullptr || sel_idx == nullptr || O == nullptr)
+    return SVG2_ERR_INVALID_ARG;
+  if (!aligned(Qp, 16) || !aligned(Kp, 16) || !aligned(Vp, 16) || !aligned(O, 16)) return SVG2_ERR_INVALID_ARG;
+  if (scale != scale) return SVG2_ERR_INVALID_ARG;
+  const int BH = B * H;
+  Carve c(ws);
+  DeviceStatus* st = c.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
+  AttnScratch a;
+  carve_attn(c, BH, N, nQ, a);
+  r = check_ws(ws, ws_bytes, c.off);
+  if (r != SVG2_OK) return r;
+  return to_status(launch_sparse_attn(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, BH, N, d, nQ, nK, scale, perm_q, O,
+                                      a, st, wait_budget_of(st), static_cast<cudaStream_t>(stream), lse));
+}
+
 int svg2_sparse_attn(const void* Qp, const void* Kp, const void* Vp, const int32_t* q_off, const int32_t* k_off,
                      const int32_t* sel_count, const int32_t* sel_idx, int B, int H, int N, int d, int nQ, int nK,
                      float scale, const int32_t* perm_q, void* O, void* ws, size_t ws_bytes, void* stream) {
   try {
-    int r = check_sizes(B, H, N, d);
-    if (r == SVG2_OK) r = check_k(nQ, N);
-    if (r == SVG2_OK) r = check_k(nK, N);
-    if (r != SVG2_OK) return r;
-    if (Qp == nullptr || Kp == nullptr || Vp == nullptr || q_off == nullptr || k_off == nullptr ||
-        sel_count == nullptr || sel_idx == nullptr || O == nullptr)
-      return SVG2_ERR_INVALID_ARG;
-    if (!aligned(Qp, 16) || !aligned(Kp, 16) || !aligned(Vp, 16) || !aligned(O, 16)) return SVG2_ERR_INVALID_ARG;
-    if (scale != scale) return SVG2_ERR_INVALID_ARG;
-    const int BH = B * H;
-    Carve c(ws);
-    DeviceStatus* st = c.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
-    AttnScratch a;
-    carve_attn(c, BH, N, nQ, a);
-    r = check_ws(ws, ws_bytes, c.off);
-    if (r != SVG2_OK) return r;
-    return to_status(launch_sparse_attn(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, BH, N, d, nQ, nK, scale, perm_q,
-                                        O, a, st, wait_budget_of(st), static_cast<cudaStream_t>(stream)));
+    return sparse_attn_call(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, B, H, N, d, nQ, nK, scale, perm_q, O, nullptr,
+                            ws, ws_bytes, stream);
+  } catch (...) {
+    return SVG2_ERR_CUDA;
+  }
+}
+
+int svg2_sparse_attn_lse(const void* Qp, const void* Kp, const void* Vp, const int32_t* q_off, const int32_t* k_off,
+                         const int32_t* sel_count, const int32_t* sel_idx, int B, int H, int N, int d, int nQ, int nK,
+                         float scale, const int32_t* perm_q, void* O, float* lse, void* ws, size_t ws_bytes,
+                         void* stream) {
+  try {
+    if (lse == nullptr || !aligned(lse, 4) || !training_scale(scale)) return SVG2_ERR_INVALID_ARG;
+    return sparse_attn_call(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, B, H, N, d, nQ, nK, scale, perm_q, O, lse, ws,
+                            ws_bytes, stream);
   } catch (...) {
     return SVG2_ERR_CUDA;
   }
@@ -493,26 +521,201 @@ int svg2_dense_attn_workspace_size(int B, int H, int N, int d, size_t* bytes) {
   return SVG2_OK;
 }
 
+static int dense_attn_call(const void* Q, const void* K, const void* V, int B, int H, int N, int d, float scale,
+                           void* O, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  int r = check_sizes(B, H, N, d);
+  if (r != SVG2_OK) return r;
+  if (Q == nullptr || K == nullptr || V == nullptr || O == nullptr) return SVG2_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16)) return SVG2_ERR_INVALID_ARG;
+  if (!finite_scale(scale)) return SVG2_ERR_INVALID_ARG;
+  const int BH = B * H;
+  Carve c(ws);
+  DenseCarve D;
+  carve_dense(c, BH, N, D);
+  r = check_ws(ws, ws_bytes, c.off);
+  if (r != SVG2_OK) return r;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_dense_plan(BH, N, D.q_off, D.k_off, D.sel_count, D.sel_idx, s);
+  if (e == cudaSuccess)
+    e = launch_sparse_attn(Q, K, V, D.q_off, D.k_off, D.sel_count, D.sel_idx, BH, N, d, 1, 1, scale, nullptr, O,
+                           D.attn, D.st, wait_budget_of(D.st), s, lse);
+  return to_status(e);
+}
+
 int svg2_dense_attn(const void* Q, const void* K, const void* V, int B, int H, int N, int d, float scale, void* O,
                     void* ws, size_t ws_bytes, void* stream) {
   try {
-    int r = check_sizes(B, H, N, d);
-    if (r != SVG2_OK) return r;
-    if (Q == nullptr || K == nullptr || V == nullptr || O == nullptr) return SVG2_ERR_INVALID_ARG;
-    if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16)) return SVG2_ERR_INVALID_ARG;
-    if (!(scale == scale) || scale == INFINITY || scale == -INFINITY) return SVG2_ERR_INVALID_ARG;
-    const int BH = B * H;
-    Carve c(ws);
+    return dense_attn_call(Q, K, V, B, H, N, d, scale, O, nullptr, ws, ws_bytes, stream);
+  } catch (...) {
+    return SVG2_ERR_CUDA;
+  }
+}
+
+int svg2_dense_attn_lse(const void* Q, const void* K, const void* V, int B, int H, int N, int d, float scale, void* O,
+                        float* lse, void* ws, size_t ws_bytes, void* stream) {
+  try {
+    if (lse == nullptr || !aligned(lse, 4) || !training_scale(scale)) return SVG2_ERR_INVALID_ARG;
+    return dense_attn_call(Q, K, V, B, H, N, d, scale, O, lse, ws, ws_bytes, stream);
+  } catch (...) {
+    return SVG2_ERR_CUDA;
+  }
+}
+
+// The workspace of an attention training step: the forward's layout or the backward's, whichever is larger
+// (the two calls use it in turn).  nQ = 0: dense.
+static size_t bwd_bytes(int BH, int N, int d, int nQ, int nK, void* ws, DeviceStatus** st, BwdScratch* sc) {
+  Carve f(nullptr);
+  if (nQ > 0) {
+    f.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
+    AttnScratch a;
+    carve_attn(f, BH, N, nQ, a);
+  } else {
     DenseCarve D;
-    carve_dense(c, BH, N, D);
+    carve_dense(f, BH, N, D);
+  }
+  Carve c(ws);
+  DeviceStatus* s = c.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
+  BwdScratch b;
+  carve_bwd(c, BH, N, d, nQ, nK, b);
+  if (st != nullptr) *st = s;
+  if (sc != nullptr) *sc = b;
+  return align_up(c.off > f.off ? c.off : f.off, 256);
+}
+
+// Checks and launch shared by the two gradient calls (nQ = 0: dense).
+static int attn_bwd_call(const BwdInputs& in, int B, int H, int N, int d, int nQ, int nK, float scale, void* ws,
+                         size_t ws_bytes, void* stream) {
+  for (const void* p : {in.Q, in.K, in.V, in.O, in.dO, static_cast<const void*>(in.dQ),
+                        static_cast<const void*>(in.dK), static_cast<const void*>(in.dV)})
+    if (p == nullptr || !aligned(p, 16)) return SVG2_ERR_INVALID_ARG;
+  if (in.lse == nullptr || !aligned(in.lse, 4) || !training_scale(scale)) return SVG2_ERR_INVALID_ARG;
+  // an output that is also an input (or another output) would be overwritten while other units read it
+  const void* outs[3] = {in.dQ, in.dK, in.dV};
+  for (int i = 0; i < 3; ++i) {
+    for (const void* p : {in.Q, in.K, in.V, in.O, in.dO})
+      if (outs[i] == p) return SVG2_ERR_INVALID_ARG;
+    if (outs[i] == outs[(i + 1) % 3]) return SVG2_ERR_INVALID_ARG;
+  }
+  DeviceStatus* st;
+  BwdScratch sc;
+  const int r = check_ws(ws, ws_bytes, bwd_bytes(B * H, N, d, nQ, nK, ws, &st, &sc));
+  if (r != SVG2_OK) return r;
+  return to_status(launch_attn_bwd(in, B * H, N, d, nQ, nK, scale, sc, st, wait_budget_of(st),
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+int svg2_dense_attn_bwd_workspace_size(int B, int H, int N, int d, size_t* bytes) {
+  if (bytes == nullptr) return SVG2_ERR_INVALID_ARG;
+  const int r = check_sizes(B, H, N, d);
+  if (r != SVG2_OK) return r;
+  *bytes = bwd_bytes(B * H, N, d, 0, 0, nullptr, nullptr, nullptr);
+  return SVG2_OK;
+}
+
+int svg2_dense_attn_bwd(const void* Q, const void* K, const void* V, const void* O, const float* lse, const void* dO,
+                        int B, int H, int N, int d, float scale, void* dQ, void* dK, void* dV, void* ws,
+                        size_t ws_bytes, void* stream) {
+  try {
+    const int r = check_sizes(B, H, N, d);
+    if (r != SVG2_OK) return r;
+    const BwdInputs in{Q, K, V, O, dO, lse, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, dQ, dK, dV};
+    return attn_bwd_call(in, B, H, N, d, 0, 0, scale, ws, ws_bytes, stream);
+  } catch (...) {
+    return SVG2_ERR_CUDA;
+  }
+}
+
+int svg2_sparse_attn_bwd_workspace_size(int B, int H, int N, int d, int nQ, int nK, size_t* bytes) {
+  if (bytes == nullptr) return SVG2_ERR_INVALID_ARG;
+  int r = check_sizes(B, H, N, d);
+  if (r == SVG2_OK) r = check_k(nQ, N);
+  if (r == SVG2_OK) r = check_k(nK, N);
+  if (r != SVG2_OK) return r;
+  *bytes = bwd_bytes(B * H, N, d, nQ, nK, nullptr, nullptr, nullptr);
+  return SVG2_OK;
+}
+
+int svg2_sparse_attn_bwd(const void* Qp, const void* Kp, const void* Vp, const void* O, const float* lse,
+                         const void* dO, const int32_t* q_off, const int32_t* k_off, const int32_t* sel_count,
+                         const int32_t* sel_idx, int B, int H, int N, int d, int nQ, int nK, float scale,
+                         const int32_t* perm_q, const int32_t* perm_k, void* dQ, void* dK, void* dV, void* ws,
+                         size_t ws_bytes, void* stream) {
+  try {
+    int r = check_sizes(B, H, N, d);
+    if (r == SVG2_OK) r = check_k(nQ, N);
+    if (r == SVG2_OK) r = check_k(nK, N);
+    if (r != SVG2_OK) return r;
+    if (q_off == nullptr || k_off == nullptr || sel_count == nullptr || sel_idx == nullptr) return SVG2_ERR_INVALID_ARG;
+    const BwdInputs in{Qp, Kp, Vp, O, dO, lse, q_off, k_off, sel_count, sel_idx, perm_q, perm_k, dQ, dK, dV};
+    return attn_bwd_call(in, B, H, N, d, nQ, nK, scale, ws, ws_bytes, stream);
+  } catch (...) {
+    return SVG2_ERR_CUDA;
+  }
+}
+
+// Checks shared by the two layer-norm calls.
+static int check_norm(const void* X, int dtype, long long rows, int width, const void* Y) {
+  if (rows < 1 || width < 1 || !valid_dtype(dtype)) return SVG2_ERR_INVALID_ARG;
+  if (rows >= (1LL << 31) || width > SVG2_MAX_NORM_WIDTH) return SVG2_ERR_UNSUPPORTED;
+  const size_t esz = dtype == SVG2_F32 ? 4 : 2;
+  if (X == nullptr || Y == nullptr || !aligned(X, esz) || !aligned(Y, esz)) return SVG2_ERR_INVALID_ARG;
+  return SVG2_OK;
+}
+
+int svg2_layer_norm(const void* X, int dtype, const float* gamma, const float* beta, long long rows, int width,
+                    float eps, void* Y, float* mean, float* rstd, void* stream) {
+  try {
+    const int r = check_norm(X, dtype, rows, width, Y);
+    if (r != SVG2_OK) return r;
+    if (!(eps >= 0.f) || eps == INFINITY) return SVG2_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(gamma), static_cast<const void*>(beta),
+                          static_cast<const void*>(mean), static_cast<const void*>(rstd)})
+      if (!aligned(p, 4)) return SVG2_ERR_INVALID_ARG;
+    NormCall n{};
+    n.X = X, n.Y = Y, n.gamma = gamma, n.beta = beta, n.mean = mean, n.rstd = rstd;
+    n.rows = rows, n.width = width, n.eps = eps;
+    return to_status(launch_norm(n, dtype == SVG2_F32, false, static_cast<cudaStream_t>(stream)));
+  } catch (...) {
+    return SVG2_ERR_CUDA;
+  }
+}
+
+static float* carve_norm(Carve& c, long long rows, int width) {
+  c.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
+  return c.take<float>(static_cast<size_t>(norm_max_parts(rows)) * 2 * width);
+}
+
+int svg2_layer_norm_bwd_workspace_size(long long rows, int width, size_t* bytes) {
+  if (bytes == nullptr || rows < 1 || width < 1) return SVG2_ERR_INVALID_ARG;
+  if (rows >= (1LL << 31) || width > SVG2_MAX_NORM_WIDTH) return SVG2_ERR_UNSUPPORTED;
+  Carve c(nullptr);
+  carve_norm(c, rows, width);
+  *bytes = align_up(c.off, 256);
+  return SVG2_OK;
+}
+
+int svg2_layer_norm_bwd(const void* X, const void* dY, int dtype, const float* gamma, const float* mean,
+                        const float* rstd, long long rows, int width, void* dX, float* dgamma, float* dbeta, void* ws,
+                        size_t ws_bytes, void* stream) {
+  try {
+    int r = check_norm(X, dtype, rows, width, dX);
+    if (r != SVG2_OK) return r;
+    if (dY == nullptr || !aligned(dY, dtype == SVG2_F32 ? 4 : 2) || mean == nullptr || rstd == nullptr)
+      return SVG2_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(gamma), static_cast<const void*>(mean),
+                          static_cast<const void*>(rstd), static_cast<const void*>(dgamma),
+                          static_cast<const void*>(dbeta)})
+      if (!aligned(p, 4)) return SVG2_ERR_INVALID_ARG;
+    if (dgamma != nullptr && dgamma == dbeta) return SVG2_ERR_INVALID_ARG;
+    Carve c(ws);
+    NormCall n{};
+    n.partial = carve_norm(c, rows, width);
     r = check_ws(ws, ws_bytes, c.off);
     if (r != SVG2_OK) return r;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_dense_plan(BH, N, D.q_off, D.k_off, D.sel_count, D.sel_idx, s);
-    if (e == cudaSuccess)
-      e = launch_sparse_attn(Q, K, V, D.q_off, D.k_off, D.sel_count, D.sel_idx, BH, N, d, 1, 1, scale, nullptr, O,
-                             D.attn, D.st, wait_budget_of(D.st), s);
-    return to_status(e);
+    n.X = X, n.dY = dY, n.Y = dX, n.gamma = gamma, n.mean = const_cast<float*>(mean);
+    n.rstd = const_cast<float*>(rstd), n.dgamma = dgamma, n.dbeta = dbeta;
+    n.rows = rows, n.width = width;
+    return to_status(launch_norm(n, dtype == SVG2_F32, true, static_cast<cudaStream_t>(stream)));
   } catch (...) {
     return SVG2_ERR_CUDA;
   }

@@ -56,6 +56,7 @@ constexpr uint32_t attn_smem() {
   return 6 * tile_bytes<D, F8>() + 1024 /*align*/ + 4096 /*ranges*/ + 4096 + 64 /*cum*/ + 256;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // Of every 16 key pairs of a row, this many (the last ones) get 2^x from the cubic on the FMA pipe;
 // the rest use the MUFU, whose 16 exponentials per clock per SM would otherwise bound the softmax.
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                        const AttnElem<F8>* __restrict__ Vp, const int32_t* __restrict__ k_off,
                        const int32_t* __restrict__ sel_count, const int32_t* __restrict__ sel_idx, int N, int nQ,
                        int nK, float scale, const int32_t* __restrict__ perm_q, __nv_bfloat16* __restrict__ O,
-                       const AttnUnit* __restrict__ units, const int32_t* __restrict__ head_base, int BH,
+                       float* __restrict__ lse, const AttnUnit* __restrict__ units, const int32_t* __restrict__ head_base, int BH,
                        const F8Scales f8, DeviceStatus* st, const uint64_t* __restrict__ wait_budget) {
   const int total_units = head_base[BH];
   if (static_cast<int>(blockIdx.x) >= total_units) return;
@@ -598,6 +599,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         uint4* dst = reinterpret_cast<uint4*>(O + (static_cast<size_t>(bh) * N + (tk < 0 ? 0 : tk)) * D);
         const float inv = (T > 0 && l > 0.f) ? (F8 ? f8.v[bh] : 1.f) / l : 0.f;
+        // log sum_j exp(s_j * scale) of the row, for the backward pass: -inf for a row that keeps no key
+        if (lse != nullptr && row < nrows_x)
+          lse[static_cast<size_t>(bh) * N + prow] = T > 0 ? (m_used + log2f(l)) * kLn2 : -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t v[32];
@@ -774,7 +778,7 @@ namespace {
 template <int D, bool F8>
 cudaError_t launch_attn_kernel(const CUtensorMap& tq, const void* Kp, const void* Vp, const int32_t* k_off,
                                const int32_t* sel_count, const int32_t* sel_idx, int BH, int N, int nQ, int nK,
-                               float scale, const int32_t* perm_q, void* O, const AttnScratch& sc,
+                               float scale, const int32_t* perm_q, void* O, float* lse, const AttnScratch& sc,
                                const F8Scales& f8, DeviceStatus* st, const uint64_t* wait_budget, cudaStream_t s) {
   constexpr uint32_t smem = attn_smem<D, F8>();
   cudaError_t e = cudaFuncSetAttribute(sparse_attn_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -782,7 +786,7 @@ cudaError_t launch_attn_kernel(const CUtensorMap& tq, const void* Kp, const void
   const long long grid = static_cast<long long>(BH) * attn_max_units_per_head(N, nQ);
   sparse_attn_kernel<D, F8><<<static_cast<unsigned>(grid), kAttnThreads, smem, s>>>(
       tq, static_cast<const AttnElem<F8>*>(Kp), static_cast<const AttnElem<F8>*>(Vp), k_off, sel_count, sel_idx, N, nQ, nK,
-      scale, perm_q, static_cast<__nv_bfloat16*>(O), sc.units, sc.head_base, BH, f8, st, wait_budget);
+      scale, perm_q, static_cast<__nv_bfloat16*>(O), lse, sc.units, sc.head_base, BH, f8, st, wait_budget);
   return cudaGetLastError();
 }
 
@@ -800,16 +804,16 @@ cudaError_t launch_sparse_attn(const void* Qp, const void* Kp, const void* Vp, c
                                const int32_t* k_off, const int32_t* sel_count, const int32_t* sel_idx, int BH,
                                int N, int d, int nQ, int nK, float scale, const int32_t* perm_q, void* O,
                                const AttnScratch& sc, DeviceStatus* st, const uint64_t* wait_budget,
-                               cudaStream_t s) {
+                               cudaStream_t s, float* lse) {
   cudaError_t e = launch_attn_plan(q_off, BH, N, nQ, sc, st, s);
   if (e != cudaSuccess) return e;
   alignas(64) CUtensorMap tq;
   e = make_tmap_bf16_rows(&tq, Qp, static_cast<uint64_t>(BH) * N, static_cast<uint32_t>(d), 128);
   if (e != cudaSuccess) return e;
   if (d == 128)
-    return launch_attn_kernel<128, false>(tq, Kp, Vp, k_off, sel_count, sel_idx, BH, N, nQ, nK, scale, perm_q, O, sc,
-                                          F8Scales{}, st, wait_budget, s);
-  return launch_attn_kernel<64, false>(tq, Kp, Vp, k_off, sel_count, sel_idx, BH, N, nQ, nK, scale, perm_q, O, sc,
+    return launch_attn_kernel<128, false>(tq, Kp, Vp, k_off, sel_count, sel_idx, BH, N, nQ, nK, scale, perm_q, O, lse,
+                                          sc, F8Scales{}, st, wait_budget, s);
+  return launch_attn_kernel<64, false>(tq, Kp, Vp, k_off, sel_count, sel_idx, BH, N, nQ, nK, scale, perm_q, O, lse, sc,
                                        F8Scales{}, st, wait_budget, s);
 }
 
@@ -824,8 +828,8 @@ cudaError_t launch_sparse_attn_fp8(const void* Qp8, const void* Kp8, const void*
   alignas(64) CUtensorMap tq;
   e = make_tmap_u8_rows(&tq, Qp8, static_cast<uint64_t>(BH) * N, static_cast<uint32_t>(d), 128);
   if (e != cudaSuccess) return e;
-  return launch_attn_kernel<128, true>(tq, Kp8, Vp8, k_off, sel_count, sel_idx, BH, N, nQ, nK, scale, perm_q, O, sc,
-                                       f8, st, wait_budget, s);
+  return launch_attn_kernel<128, true>(tq, Kp8, Vp8, k_off, sel_count, sel_idx, BH, N, nQ, nK, scale, perm_q, O,
+                                       nullptr, sc, f8, st, wait_budget, s);
 }
 
 cudaError_t launch_selftest_mma(const void* A, const void* Bm, int n, const void* V, float* C, float* O,

@@ -1,0 +1,801 @@
+// Gradients of the dense and the variable-block sparse attention on tcgen05 tensor cores.
+//
+// With s_ij = scale q_i.k_j, P_ij = exp(s_ij - lse_i) (the forward's probabilities, recomputed from its
+// log-sum-exp, so no maximum is needed) and delta_i = dO_i.O_i:
+//   dV = P^T dO,   dS = P o (dO V^T - delta),   dK = scale dS^T Q,   dQ = scale dS K.
+// dK, dV sum over queries and dQ over keys, so the work is cut into two kinds of unit, both with 128
+// resident rows and a stream of 128-row tiles, and every output row has one owner: no atomics, the
+// same bits on every run, no float32 copy of dQ in memory.  The price is that S and dP are computed
+// twice (7 products per tile pair where one pass with atomic dQ sums would take 5).
+//   key unit    K, V of 128 rows of one K cluster stay in shared memory; Q, dO of the Q clusters that
+//               keep it stream by.  S^T = K Q^T, dP^T = V dO^T; P^T and dS^T go back to TMEM as the A
+//               operands of dV += P^T dO and dK += dS^T Q.
+//   query unit  Q, dO of 128 rows of one Q cluster stay; K, V of its kept clusters stream by.
+//               S = Q K^T, dP = dO V^T; dS goes back to TMEM as the A operand of dQ += dS K.
+// The streams are packed as in the forward: the kept clusters' rows back to back, so ragged cluster
+// edges cost no padding.  A tile is fetched by TMA in boxes of power-of-two heights, one run of boxes
+// per contiguous piece, the rows past the stream's end from outside the tensor (zero fill).
+//   warps 0-7   P and dS: TMEM lanes = resident rows, warps 0-3 the tile's columns 0-63, 4-7 64-127
+//   warp 8      TMEM allocator and MMA issuer
+//   warp 9      range table, then TMA producer (and the streamed queries' lse and delta by cp.async)
+// P and dS are rounded to bf16 for the products (as P is in the forward); both stay float32 until then.
+// A row of dS sums to zero, so dQ does not depend on what all keys have in common; the rounded dS, with delta
+// from a bf16 O, sums to some r_i instead, and dQ would carry scale r_i times that common part, which
+// in a trained K is often its largest.  The query unit therefore sums the dS values it hands over and
+// subtracts scale r_i c, c = the mean key (any c is right in exact arithmetic): on keys with a mean of
+// four standard deviations the error of dQ falls from 1.0e-2 to 2.6e-3 of its norm.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include "svg2_device.cuh"
+#include "svg2_internal.h"
+
+namespace svg2 {
+
+namespace {
+
+// 12 warps in three warpgroups: 8 for P and dS, then the MMA and producer warps (10 and 11 idle).
+constexpr int kBwdThreads = 384;
+// Register split after set-up (setmaxnreg): 256 x 176 + 128 x 152 = 64512 = 384 x 168, the launch's
+// allocation under __launch_bounds__(384, 1).  The one split in steps of 8 at which neither side spills
+// (168: the P and dS loop does; 184: the MMA warp's descriptors do).
+constexpr int kBwdLaunchRegs = 168, kBwdSoftmaxRegs = 176, kBwdOtherRegs = 152;
+static_assert(256 * kBwdSoftmaxRegs + (kBwdThreads - 256) * kBwdOtherRegs <= kBwdThreads * kBwdLaunchRegs,
+              "register split");
+constexpr int kBwdMmaWarp = 8, kBwdProducerWarp = 9;
+constexpr int kBwdMaxRanges = 1024;
+constexpr int kBwdBoxes = 8;  // box heights 1, 2, ..., 128
+constexpr float kLog2e = 1.4426950408889634f;
+// Of every 16 column pairs, this many get 2^x from the cubic on the FMA pipe, the rest from the MUFU.
+constexpr int kBwdCubicPairs = 4;
+
+template <int D>
+constexpr uint32_t bwd_tile_bytes() { return 128u * D * 2u; }
+template <int D>
+constexpr uint32_t bwd_smem() {
+  return 6 * bwd_tile_bytes<D>() + 1024 /*align*/ + 4 * 512 /*lse, delta of two stages*/ + 4096 /*range starts*/ +
+         4096 + 64 /*range offsets*/ + 256 /*barriers*/;
+}
+
+struct BwdMaps {  // [Q, K, V, dO][log2 box height], 64 columns wide, 128-byte swizzle
+  CUtensorMap m[4][kBwdBoxes];
+};
+
+struct BwdArgs {
+  const int32_t *q_off, *k_off, *sel_count, *sel_idx;  // null: dense
+  const uint32_t* keepers;                             // [BH, nK, W] bit i: Q cluster i keeps this K cluster
+  const BwdUnit *k_units, *q_units;                    // [BH, per_head]
+  const int32_t *perm_q, *perm_k;
+  const float *neg_lse2, *neg_delta;                   // [BH, N] -lse log2(e), -delta, by permuted row
+  const float* k_mean;                                 // [BH, D]
+  __nv_bfloat16 *dQ, *dK, *dV;
+  int BH, N, nQ, nK, W, k_per_head, q_per_head;
+  float scale;
+  DeviceStatus* st;
+  const uint64_t* wait_budget;
+};
+
+struct BwdBars {
+  uint64_t res_full, t1_full[2], t2_full[2], t1_empty[2], t2_empty[2], s_full[2], p_full, dp_full, ds_full, o_full,
+      mma_done;
+  uint32_t tmem_base;
+  int32_t L, nranges;
+};
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return d;
+}
+
+// 4-byte asynchronous copy; bytes = 0 writes a zero and reads nothing.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// ------------------------------------------------------------------------------------------------
+// delta_i = dO_i . O_i and the scaled log-sum-exp, by permuted row; with perm, dO's rows in permuted
+// order too.  D / 8 lanes per row, 16 bytes each: bound by the reads of O and dO.  The CTAs past row_ctas
+// take the mean of up to kMeanRows evenly spaced K rows of one plane each.
+// ------------------------------------------------------------------------------------------------
+constexpr int kMeanRows = 512;
+
+template <int D>
+__device__ void mean_key(const uint4* __restrict__ K, int bh, int N, float* __restrict__ k_mean) {
+  constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
+  __shared__ float part[kGroups][D];
+  const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int S = min(N, kMeanRows);
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int t = group; t < S; t += kGroups) {
+    const long long row = static_cast<long long>(bh) * N + static_cast<long long>(t) * N / S;
+    const uint4 w = __ldg(K + row * kLanes + sub);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[2 * e] += bf16lo_to_f32(u[e]), acc[2 * e + 1] += bf16hi_to_f32(u[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) part[group][sub * 8 + e] = acc[e];
+  __syncthreads();
+  for (int c = threadIdx.x; c < D; c += 256) {
+    float s = 0.f;
+    for (int g = 0; g < kGroups; ++g) s += part[g][c];
+    s /= static_cast<float>(S);
+    k_mean[static_cast<size_t>(bh) * D + c] = fabsf(s) < INFINITY ? s : 0.f;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__ O, const uint4* __restrict__ dO,
+                                                       const float* __restrict__ lse, const int32_t* __restrict__ perm,
+                                                       const uint4* __restrict__ K, int N, long long rows,
+                                                       int row_ctas, float* __restrict__ neg_lse2,
+                                                       float* __restrict__ neg_delta, uint4* __restrict__ dOp,
+                                                       float* __restrict__ k_mean, DeviceStatus* st) {
+  if (static_cast<int>(blockIdx.x) >= row_ctas) {
+    mean_key<D>(K, blockIdx.x - row_ctas, N, k_mean);
+    return;
+  }
+  constexpr int kLanes = D / 8;
+  const int sub = threadIdx.x % kLanes;
+  const long long step = static_cast<long long>(row_ctas) * (256 / kLanes);
+  const long long first = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+  // every lane of a warp takes part in the shuffles: rows past the end only skip their memory
+  for (long long r0 = first - (threadIdx.x % 32) / kLanes; r0 < rows; r0 += step) {
+    const long long r = r0 + (threadIdx.x % 32) / kLanes;
+    const bool in = r < rows;
+    long long src = r;
+    bool valid = in;
+    if (in && perm != nullptr) {
+      const long long bh = r / N;
+      const int t = perm[r];
+      SVG2_DEBUG_CHECK(t >= 0 && t < N, st, kWhereGather, r, t);
+      valid = t >= 0 && t < N;  // a bad entry has no output row, so no gradient either
+      src = bh * N + t;
+    }
+    uint4 o = make_uint4(0, 0, 0, 0), g = make_uint4(0, 0, 0, 0);
+    if (valid) {
+      o = O[src * kLanes + sub];
+      g = dO[src * kLanes + sub];
+    }
+    float acc = 0.f;
+    const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      acc = fmaf(bf16lo_to_f32(ow[e]), bf16lo_to_f32(gw[e]), acc);
+      acc = fmaf(bf16hi_to_f32(ow[e]), bf16hi_to_f32(gw[e]), acc);
+    }
+#pragma unroll
+    for (int s = kLanes / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
+    if (in) {
+      if (dOp != nullptr) dOp[r * kLanes + sub] = g;
+      if (sub == 0) {
+        const float l = lse[r];
+        neg_lse2[r] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row without keys has P = 0
+        neg_delta[r] = -acc;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// The sparse plan, one CTA per (b,h): which Q clusters keep each K cluster (the transposed selection,
+// as bits), and the units of both kinds.  A K cluster listed twice for one Q cluster, or an index out
+// of range, latches SVG2_ERR_DEVICE_BOUNDS: the gradient kernel then does nothing.
+// ------------------------------------------------------------------------------------------------
+__device__ void write_units(const int32_t* off, int n, int N, int per_head, BwdUnit* out, int32_t* count,
+                            DeviceStatus* st) {
+  // count[i] = exclusive prefix of the clusters' 128-row units
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int r0 = off[i], len = off[i + 1] - r0;
+    const bool ok = r0 >= 0 && len > 0 && r0 <= N - len;
+    SVG2_DEBUG_CHECK(ok || len == 0, st, kWherePlan, i, r0);
+    count[i] = ok ? (len + 127) / 128 : 0;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int run = 0;
+    for (int b = 0; b < n; b += 32) {
+      const int i = b + threadIdx.x;
+      const int v = i < n ? count[i] : 0;
+      int incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (static_cast<int>(threadIdx.x) >= o) incl += u;
+      }
+      if (i < n) count[i] = run + incl - v;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (threadIdx.x == 0) count[n] = run;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int r0 = off[i], len = off[i + 1] - r0;
+    const int units = count[i + 1] - count[i];
+    for (int u = 0; u < units; ++u) {
+      const int slot = count[i] + u;
+      if (slot < per_head) out[slot] = BwdUnit{i, r0 + u * 128, min(128, len - u * 128)};
+    }
+  }
+  for (int s = count[n] + threadIdx.x; s < per_head; s += blockDim.x) out[s] = BwdUnit{0, 0, 0};
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(512) bwd_plan_kernel(const int32_t* __restrict__ q_off,
+                                                       const int32_t* __restrict__ k_off,
+                                                       const int32_t* __restrict__ sel_count,
+                                                       const int32_t* __restrict__ sel_idx, int N, int nQ, int nK,
+                                                       int W, uint32_t* __restrict__ keepers,
+                                                       BwdUnit* __restrict__ k_units, int k_per_head,
+                                                       BwdUnit* __restrict__ q_units, int q_per_head,
+                                                       DeviceStatus* st) {
+  extern __shared__ uint32_t bits[];  // [nK, W]
+  __shared__ int32_t count[kMaxClustersAssign + 1];
+  const int bh = blockIdx.x;
+  for (int w = threadIdx.x; w < nK * W; w += blockDim.x) bits[w] = 0u;
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = warp; i < nQ; i += static_cast<int>(blockDim.x >> 5)) {
+    const size_t row = static_cast<size_t>(bh) * nQ + i;
+    const int cnt = sel_count[row];
+    if (cnt < 0 || cnt > nK) {
+      if (lane == 0) raise_status(st, kStatusDeviceBounds, kWherePlan, i, cnt);
+      continue;
+    }
+    for (int e = lane; e < cnt; e += 32) {
+      const int j = sel_idx[row * nK + e];
+      const uint32_t bit = 1u << (i & 31);
+      if (j < 0 || j >= nK || (atomicOr(&bits[j * W + (i >> 5)], bit) & bit) != 0u)
+        raise_status(st, kStatusDeviceBounds, kWherePlan, i, j);
+    }
+  }
+  __syncthreads();
+  for (int w = threadIdx.x; w < nK * W; w += blockDim.x) keepers[static_cast<size_t>(bh) * nK * W + w] = bits[w];
+  write_units(k_off + static_cast<size_t>(bh) * (nK + 1), nK, N, k_per_head,
+              k_units + static_cast<size_t>(bh) * k_per_head, count, st);
+  write_units(q_off + static_cast<size_t>(bh) * (nQ + 1), nQ, N, q_per_head,
+              q_units + static_cast<size_t>(bh) * q_per_head, count, st);
+}
+
+// ------------------------------------------------------------------------------------------------
+// One unit.  KV: a key unit (dK, dV), else a query unit (dQ).  R1, R2: resident tiles (K, V | Q, dO);
+// T1, T2: streamed tiles (Q, dO | K, V).
+// ------------------------------------------------------------------------------------------------
+// TMEM columns: S (the query unit alternates between two slots), dP, and the accumulators.  P and dS
+// (bf16) overwrite their S and dP: column half h puts its 64 values at the half's first 32 columns, which
+// only its own warps have read.
+template <bool KV>
+struct BwdTmem {
+  static constexpr uint32_t s1 = 128;                 // query unit: second S slot
+  static constexpr uint32_t acc1 = 128;               // key unit: dV
+  static constexpr uint32_t dp = 256, acc2 = 384;     // acc2: dK | dQ
+};
+
+template <int D, bool KV>
+__device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, const BwdUnit un, const int bh,
+                                         uint8_t* smem, BwdBars* bars, float* stats, const int32_t* r_start,
+                                         const int32_t* r_cum, const long long wb) {
+  constexpr uint32_t kTile = bwd_tile_bytes<D>();
+  constexpr int kHalves = D / 64;   // 128-byte swizzle atoms across a row
+  constexpr int kSteps = D / 16;    // instructions of one S or dP product
+  using Tm = BwdTmem<KV>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t tmem = bars->tmem_base;
+  const int L = bars->L;
+  const int T = (L + 127) / 128;
+  const bool dense = a.sel_idx == nullptr;
+  DeviceStatus* st = a.st;
+  const uint32_t r1 = smem_u32(smem), r2 = r1 + kTile, t1 = r1 + 2 * kTile, t2 = r1 + 4 * kTile;
+
+  if (warp == kBwdMmaWarp) {
+    if (elect_one() && T > 0) {
+      const uint32_t id_s = idesc_bf16_f32(128, 128, 0);  // both operands K-major
+      const uint32_t id_o = idesc_bf16_f32(128, D, 1);    // B = a streamed tile read row-major (MN-major)
+      // D[slot] = R x T^T, contraction over d
+      auto product = [&](uint32_t d_tmem, uint32_t ra, uint32_t tb) {
+        const uint64_t da = sdesc_sw128(ra, 16, 1024), db = sdesc_sw128(tb, 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < kSteps; ++ks) {
+          const uint64_t off = static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
+          mma_ss(d_tmem, da + off, db + off, id_s, ks > 0 ? 1u : 0u);
+        }
+      };
+      // acc (+)= X T with X (P or dS, bf16) in TMEM, contraction over the tile's 128 rows
+      auto accumulate = [&](uint32_t acc, uint32_t x, uint32_t tb, bool add) {
+        const uint64_t db = sdesc_sw128(tb, 16384, 1024);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_ts(acc, x + (ks >> 2) * 64 + (ks & 3) * 8, db + static_cast<uint64_t>((ks * 16 * 128) >> 4), id_o,
+                 (add || ks > 0) ? 1u : 0u);
+      };
+      auto wait = [&](uint64_t* bar, int phase) {
+        return mbar_wait(smem_u32(bar), phase & 1, st, kWhereAttnBwdMma, wb);
+      };
+      bool ok = wait(&bars->res_full, 0) && wait(&bars->t1_full[0], 0);
+      if (ok) {
+        tc_fence_after();
+        product(tmem, r1, t1);
+        mma_commit(smem_u32(&bars->s_full[0]));
+        ok = wait(&bars->t2_full[0], 0);
+      }
+      if (ok) {
+        tc_fence_after();
+        product(tmem + Tm::dp, r2, t2);
+        mma_commit(smem_u32(&bars->dp_full));
+        if (!KV) mma_commit(smem_u32(&bars->t2_empty[0]));
+      }
+      for (int j = 0; j < T && ok; ++j) {
+        const int sg = j & 1, ng = sg ^ 1;
+        const bool more = j + 1 < T;
+        if constexpr (KV) {
+          ok = wait(&bars->p_full, j);
+          if (!ok) break;
+          tc_fence_after();
+          accumulate(tmem + Tm::acc1, tmem, t2 + sg * kTile, j > 0);  // dV += P^T dO
+          mma_commit(smem_u32(&bars->t2_empty[sg]));
+        }
+        if (more) {
+          // key unit: the products run in issue order, so S(j+1) overwrites P(j) only after dV has read it;
+          // query unit: the other slot, whose S(j-1) was read before dS(j-1) was handed over
+          ok = wait(&bars->t1_full[ng], (j + 1) >> 1);
+          if (!ok) break;
+          tc_fence_after();
+          product(tmem + (KV ? 0u : ng * Tm::s1), r1, t1 + ng * kTile);
+          mma_commit(smem_u32(&bars->s_full[KV ? 0 : ng]));
+        }
+        ok = wait(&bars->ds_full, j);
+        if (!ok) break;
+        tc_fence_after();
+        accumulate(tmem + Tm::acc2, tmem + Tm::dp, t1 + sg * kTile, j > 0);  // dK += dS^T Q | dQ += dS K
+        mma_commit(smem_u32(&bars->t1_empty[sg]));
+        if (more) {
+          ok = wait(&bars->t2_full[ng], (j + 1) >> 1);
+          if (!ok) break;
+          tc_fence_after();
+          product(tmem + Tm::dp, r2, t2 + ng * kTile);
+          mma_commit(smem_u32(&bars->dp_full));
+          if (!KV) mma_commit(smem_u32(&bars->t2_empty[ng]));
+        }
+      }
+      if (ok) mma_commit(smem_u32(&bars->o_full));
+      mma_commit(smem_u32(&bars->mma_done));
+      mbar_wait(smem_u32(&bars->mma_done), 0, nullptr, kWhereAttnBwdMma, kWaitBudgetCycles / 8);
+    }
+  } else if (warp == kBwdProducerWarp) {
+    const bool leader = elect_one();
+    const CUtensorMap* m1 = maps.m[KV ? 0 : 1];
+    const CUtensorMap* m2 = maps.m[KV ? 3 : 2];
+    if (leader && T > 0) {
+      const uint32_t bar = smem_u32(&bars->res_full);
+      mbar_arrive_expect_tx(bar, 2 * kTile);
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        tma_load_3d(r1 + h * 16384, &maps.m[KV ? 1 : 0][7], h * 64, un.row0, bh, bar);
+        tma_load_3d(r2 + h * 16384, &maps.m[KV ? 2 : 3][7], h * 64, un.row0, bh, bar);
+      }
+    }
+    // rows [at, at + n) of a tile <- rows [row, row + n) of the plane (row = N: zeros), in boxes
+    auto fetch = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int at, int n, int row) {
+      while (n > 0) {
+        const int b = 31 - __clz(n);
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * 16384 + at * 128, &m[b], h * 64, row, bh, bar);
+        at += 1 << b;
+        n -= 1 << b;
+        if (row < a.N) row += 1 << b;
+      }
+    };
+    // calls f(first tile row, rows, first plane row) for the pieces of tile j; e: the range that holds its first row
+    auto pieces = [&](int j, int& e, auto&& f) {
+      int p = j * 128, at = 0;
+      if (dense) {  // one box: its rows past the plane's end are zero-filled
+        f(0, 128, p);
+        return;
+      }
+      while (at < 128 && p < L) {
+        while (r_cum[e + 1] <= p) ++e;
+        const int n = min(r_cum[e + 1] - p, 128 - at);
+        f(at, n, r_start[e] + (p - r_cum[e]));
+        at += n;
+        p += n;
+      }
+      if (at < 128) f(at, 128 - at, a.N);
+    };
+    int e1 = 0, e2 = 0;
+    int n1 = 0, n2 = 0;  // tiles requested of each streamed operand
+    bool ok = true;
+    const float* nl = a.neg_lse2 + static_cast<size_t>(bh) * a.N;
+    const float* nd = a.neg_delta + static_cast<size_t>(bh) * a.N;
+    for (int j = 0; j < T; ++j) {
+      const int sg = j & 1;
+      const uint32_t b1 = smem_u32(&bars->t1_full[sg]), b2 = smem_u32(&bars->t2_full[sg]);
+      if (j >= 2) {
+        ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&bars->t1_empty[sg]), ((j >> 1) - 1) & 1, st,
+                                                     kWhereAttnBwdProducer, 32, wb));
+        if (!ok) break;
+      }
+      if (leader) mbar_arrive_expect_tx(b1, kTile);
+      __syncwarp();
+      pieces(j, e1, [&](int at, int n, int row) {
+        if (leader) fetch(m1, t1 + sg * kTile, b1, at, n, row);
+        if constexpr (KV) {
+          for (int x = lane; x < n; x += 32) {
+            const bool in = row + x < a.N;  // past the stream's end: 0, and the column is masked
+            const uint32_t dst = smem_u32(stats + sg * 256 + at + x);
+            cp_async4(dst, nl + (in ? row + x : 0), in ? 4u : 0u);
+            cp_async4(dst + 512, nd + (in ? row + x : 0), in ? 4u : 0u);
+          }
+        }
+      });
+      if constexpr (KV) cp_async_mbar_arrive(b1);
+      n1 = j + 1;
+      if (j >= 2) {
+        ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&bars->t2_empty[sg]), ((j >> 1) - 1) & 1, st,
+                                                     kWhereAttnBwdProducer, 32, wb));
+        if (!ok) break;
+      }
+      if (leader) mbar_arrive_expect_tx(b2, kTile);
+      __syncwarp();
+      pieces(j, e2, [&](int at, int n, int row) {
+        if (leader) fetch(m2, t2 + sg * kTile, b2, at, n, row);
+      });
+      n2 = j + 1;
+    }
+    // Every copy has landed before the CTA leaves, also when some agent gave up: the last phase of each
+    // stage's barrier is awaited here (older phases are complete, or the stage would not have been reused).
+    cp_async_wait<0>();
+    if (leader && T > 0) {
+      const long long drain = kWaitBudgetCycles / 8;
+      mbar_wait(smem_u32(&bars->res_full), 0, nullptr, kWhereAttnBwdProducer, drain);
+#pragma unroll
+      for (int sg = 0; sg < 2; ++sg) {
+        const int f1 = (n1 + 1 - sg) >> 1, f2 = (n2 + 1 - sg) >> 1;  // fills of this stage
+        if (f1 > 0) mbar_wait(smem_u32(&bars->t1_full[sg]), (f1 - 1) & 1, nullptr, kWhereAttnBwdProducer, drain);
+        if (f2 > 0) mbar_wait(smem_u32(&bars->t2_full[sg]), (f2 - 1) & 1, nullptr, kWhereAttnBwdProducer, drain);
+      }
+    }
+  } else if (warp < 8) {
+    // ---------------- P and dS, then the unit's rows of the gradients ----------------
+    const int half = warp >> 2;  // columns 64 half .. 64 half + 63 of every tile
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float sl2 = a.scale * kLog2e;
+    const float2 scl = make_float2(sl2, sl2);
+    const size_t plane = static_cast<size_t>(bh) * a.N;
+    float nl_row = 0.f, nd_row = 0.f;
+    if (!KV && row < un.nrows) {
+      nl_row = a.neg_lse2[plane + un.row0 + row];
+      nd_row = a.neg_delta[plane + un.row0 + row];
+    }
+    auto wait = [&](uint64_t* bar, int phase) {
+      return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, st, kWhereAttnBwdSoftmax, wb));
+    };
+    float2 r_sum = make_float2(0.f, 0.f);  // query unit: this half's sum of the row's rounded dS
+    bool ok = true;
+    for (int j = 0; j < T; ++j) {
+      const int sg = j & 1;
+      const float* st_l = stats + sg * 256 + half * 64;  // key unit: -lse log2(e) of this half's columns,
+      const float* st_d = st_l + 128;                    // and -delta
+      ok = KV ? wait(&bars->s_full[0], j) : wait(&bars->s_full[sg], j >> 1);
+      if (ok && KV) ok = wait(&bars->t1_full[sg], j >> 1);  // the copies of lse and delta (already complete)
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t_s = tmem + lane_off + (KV ? 0u : sg * Tm::s1) + half * 64;
+      const uint32_t t_dp = tmem + lane_off + Tm::dp + half * 64;
+      uint32_t sv[64];
+      tmem_ld32p(t_s, sv);
+      tmem_ld32p(t_s + 32, sv + 32);
+      tmem_wait_ld();
+      const int valid = L - j * 128 - half * 64;
+      if (valid < 64) {  // past the stream's end: P = 0
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (e >= valid) sv[e] = __float_as_uint(-INFINITY);
+      }
+      // P = 2^(s log2(e) - lse log2(e))
+      float2 p[32];
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        float4 l4;
+        if constexpr (KV) l4 = *reinterpret_cast<const float4*>(st_l + 2 * e);
+        else l4 = make_float4(nl_row, nl_row, nl_row, nl_row);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float2 t = fma2(make_float2(__uint_as_float(sv[2 * (e + u)]), __uint_as_float(sv[2 * (e + u) + 1])), scl,
+                                u == 0 ? make_float2(l4.x, l4.y) : make_float2(l4.z, l4.w));
+          p[e + u] = (((e + u) & 15) >= 16 - kBwdCubicPairs) ? exp2_cubic2(t)
+                                                             : make_float2(fast_exp2(t.x), fast_exp2(t.y));
+        }
+      }
+      if constexpr (KV) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(p[e].x, p[e].y);
+        tmem_st32(t_s, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
+      }
+      ok = wait(&bars->dp_full, j);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32p(t_dp, sv);
+      tmem_ld32p(t_dp + 32, sv + 32);
+      tmem_wait_ld();
+      uint32_t dk[32];
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) {
+        float4 d4;
+        if constexpr (KV) d4 = *reinterpret_cast<const float4*>(st_d + 2 * e);
+        else d4 = make_float4(nd_row, nd_row, nd_row, nd_row);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float2 ds =
+              mul2(p[e + u], add2(make_float2(__uint_as_float(sv[2 * (e + u)]), __uint_as_float(sv[2 * (e + u) + 1])),
+                                  u == 0 ? make_float2(d4.x, d4.y) : make_float2(d4.z, d4.w)));
+          dk[e + u] = pack_bf16x2(ds.x, ds.y);
+        }
+      }
+      tmem_st32(t_dp, dk);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
+      if constexpr (!KV) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r_sum = add2(r_sum, make_float2(bf16lo_to_f32(dk[e]), bf16hi_to_f32(dk[e])));
+      }
+    }
+    float r_row = 0.f;
+    if constexpr (!KV) {  // both halves' sums (the streamed lse buffer is free in a query unit)
+      stats[half * 128 + row] = r_sum.x + r_sum.y;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      r_row = stats[row] + stats[128 + row];
+    }
+    if (ok && T > 0) ok = wait(&bars->o_full, 0);
+    if (ok) {
+      tc_fence_after();
+      // key unit: warps 0-3 write dV, warps 4-7 dK; query unit: each half of the columns of dQ
+      const int32_t* perm = KV ? a.perm_k : a.perm_q;
+      __nv_bfloat16* out = KV ? (half == 0 ? a.dV : a.dK) : a.dQ;
+      const float f = KV && half == 0 ? 1.f : a.scale;
+      constexpr int kChunks = KV ? D / 32 : D / 64;  // 32-column chunks per warp
+      const int c0 = KV ? 0 : half * kChunks;
+      const uint32_t t_o = tmem + lane_off + (KV && half == 0 ? Tm::acc1 : Tm::acc2);
+      int tk = -1;
+      if (row < un.nrows) {
+        tk = perm != nullptr ? __ldg(perm + plane + un.row0 + row) : un.row0 + row;
+        SVG2_DEBUG_CHECK(tk >= 0 && tk < a.N, st, kWhereAttnBwdSoftmax, un.row0 + row, tk);
+        if (tk < 0 || tk >= a.N) tk = -1;  // an invalid permutation entry is skipped
+      }
+      uint4* dst = reinterpret_cast<uint4*>(out + (plane + (tk < 0 ? 0 : tk)) * D);
+#pragma unroll 1
+      for (int c = c0; c < c0 + kChunks; ++c) {
+        uint32_t v[32];
+        if (T > 0) {
+          tmem_ld32(t_o + c * 32, v);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0u;
+        }
+        if constexpr (!KV) {
+          const float4* mean4 = reinterpret_cast<const float4*>(a.k_mean + static_cast<size_t>(bh) * D + c * 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 m = __ldg(mean4 + e);
+            v[4 * e + 0] = __float_as_uint(fmaf(-r_row, m.x, __uint_as_float(v[4 * e + 0])));
+            v[4 * e + 1] = __float_as_uint(fmaf(-r_row, m.y, __uint_as_float(v[4 * e + 1])));
+            v[4 * e + 2] = __float_as_uint(fmaf(-r_row, m.z, __uint_as_float(v[4 * e + 2])));
+            v[4 * e + 3] = __float_as_uint(fmaf(-r_row, m.w, __uint_as_float(v[4 * e + 3])));
+          }
+        }
+        if (tk >= 0) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(v[8 * e + 0]) * f, __uint_as_float(v[8 * e + 1]) * f);
+            w.y = pack_bf16x2(__uint_as_float(v[8 * e + 2]) * f, __uint_as_float(v[8 * e + 3]) * f);
+            w.z = pack_bf16x2(__uint_as_float(v[8 * e + 4]) * f, __uint_as_float(v[8 * e + 5]) * f);
+            w.w = pack_bf16x2(__uint_as_float(v[8 * e + 6]) * f, __uint_as_float(v[8 * e + 7]) * f);
+            dst[c * 4 + e] = w;
+          }
+        }
+      }
+    }
+  }
+}
+
+// The ranges of plane rows that a unit's stream is made of (warp 9): start rows and the exclusive
+// prefix of their lengths.
+__device__ __forceinline__ void build_ranges(const BwdArgs& a, const BwdUnit un, int bh, bool kv, int32_t* r_start,
+                                             int32_t* r_cum, BwdBars* bars) {
+  const int lane = threadIdx.x & 31;
+  const int32_t* off = kv ? a.q_off + static_cast<size_t>(bh) * (a.nQ + 1) : a.k_off + static_cast<size_t>(bh) * (a.nK + 1);
+  int cnt = 0;
+  if (kv) {  // the set bits of this K cluster's row
+    uint32_t w = lane < a.W ? a.keepers[(static_cast<size_t>(bh) * a.nK + un.cluster) * a.W + lane] : 0u;
+    const int mine = __popc(w);
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    cnt = __shfl_sync(0xffffffffu, incl, 31);
+    for (int e = incl - mine; w != 0u; ++e, w &= w - 1) r_start[e] = lane * 32 + __ffs(w) - 1;
+  } else {
+    const size_t row = static_cast<size_t>(bh) * a.nQ + un.cluster;
+    cnt = a.sel_count[row];  // the plan kernel has checked the count and the indices
+    for (int e = lane; e < cnt; e += 32) r_start[e] = a.sel_idx[row * a.nK + e];
+  }
+  __syncwarp();
+  int run = 0;
+  for (int b = 0; b < cnt; b += 32) {
+    int s0 = 0, len = 0;
+    if (b + lane < cnt) {
+      const int i = r_start[b + lane];
+      s0 = off[i];
+      len = off[i + 1] - s0;
+      if (s0 < 0 || len < 0 || s0 > a.N - len) s0 = len = 0;  // malformed offsets hold no rows
+    }
+    int incl = len;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (b + lane < cnt) {
+      r_start[b + lane] = s0;
+      r_cum[b + lane] = run + incl - len;
+    }
+    run += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) {
+    r_cum[cnt] = run;
+    bars->L = run;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs a) {
+  if (__syncthreads_or(status_set(a.st))) return;  // the whole CTA, or none of it
+  // key units first (they are the longer ones), then query units
+  const int nk = a.BH * a.k_per_head;
+  const bool kv = static_cast<int>(blockIdx.x) < nk;
+  const int idx = kv ? blockIdx.x : blockIdx.x - nk;
+  const int per = kv ? a.k_per_head : a.q_per_head;
+  const int bh = idx / per, u = idx % per;
+  const bool dense = a.sel_idx == nullptr;
+  BwdUnit un;
+  if (dense) un = BwdUnit{0, u * 128, min(128, a.N - u * 128)};
+  else un = (kv ? a.k_units : a.q_units)[idx];
+  if (un.nrows <= 0) return;
+  const long long wb = effective_wait_budget(a.wait_budget);
+
+  constexpr uint32_t kTile = bwd_tile_bytes<D>();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* stats = reinterpret_cast<float*>(smem + 6 * kTile);  // [stage][lse | delta][128]
+  int32_t* r_start = reinterpret_cast<int32_t*>(stats + 512);
+  int32_t* r_cum = r_start + kBwdMaxRanges;  // kBwdMaxRanges + 1 entries
+  BwdBars* bars = reinterpret_cast<BwdBars*>(r_cum + kBwdMaxRanges + 16);
+  const int warp = threadIdx.x >> 5;
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bars->res_full), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars->t1_full[i]), kv ? 33 : 1);  // the bytes, and each producer lane's small copies
+      mbar_init(smem_u32(&bars->t2_full[i]), 1);
+      mbar_init(smem_u32(&bars->t1_empty[i]), 1);
+      mbar_init(smem_u32(&bars->t2_empty[i]), 1);
+      mbar_init(smem_u32(&bars->s_full[i]), 1);
+    }
+    mbar_init(smem_u32(&bars->p_full), 8);
+    mbar_init(smem_u32(&bars->dp_full), 1);
+    mbar_init(smem_u32(&bars->ds_full), 8);
+    mbar_init(smem_u32(&bars->o_full), 1);
+    mbar_init(smem_u32(&bars->mma_done), 1);
+    fence_mbar_init();
+  }
+  if (warp == kBwdMmaWarp) {
+    tmem_alloc(smem_u32(&bars->tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (warp == kBwdProducerWarp) {
+    if (!dense) build_ranges(a, un, bh, kv, r_start, r_cum, bars);
+    else if ((threadIdx.x & 31) == 0) bars->L = a.N;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwdOtherRegs) : "memory");
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwdSoftmaxRegs) : "memory");
+  if (kv) bwd_unit<D, true>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, wb);
+  else bwd_unit<D, false>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, wb);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kBwdMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(bars->tmem_base, 512);
+  }
+}
+
+template <int D>
+cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float scale, const BwdScratch& sc,
+                       DeviceStatus* st, const uint64_t* wait_budget, cudaStream_t s) {
+  const bool dense = in.sel_idx == nullptr;
+  const long long rows = static_cast<long long>(BH) * N;
+  constexpr int kRows = 256 / (D / 8);  // rows per CTA pass
+  const unsigned grid = static_cast<unsigned>(rows / kRows + 1 < 148 * 16 ? rows / kRows + 1 : 148 * 16);
+  bwd_prep_kernel<D><<<grid + BH, 256, 0, s>>>(static_cast<const uint4*>(in.O), static_cast<const uint4*>(in.dO),
+                                               in.lse, in.perm_q, static_cast<const uint4*>(in.K), N, rows,
+                                               static_cast<int>(grid), sc.neg_lse2, sc.neg_delta,
+                                               in.perm_q != nullptr ? static_cast<uint4*>(sc.dOp) : nullptr,
+                                               sc.k_mean, st);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  BwdArgs a{};
+  a.BH = BH;
+  a.N = N;
+  a.nQ = nQ;
+  a.nK = nK;
+  a.W = (nQ + 31) / 32;
+  a.k_per_head = dense ? (N + 127) / 128 : bwd_max_units_per_head(N, nK);
+  a.q_per_head = dense ? (N + 127) / 128 : bwd_max_units_per_head(N, nQ);
+  if (!dense) {
+    const uint32_t bits = static_cast<uint32_t>(nK) * a.W * 4;
+    e = cudaFuncSetAttribute(bwd_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 131072);
+    if (e != cudaSuccess) return e;
+    bwd_plan_kernel<<<BH, 512, bits, s>>>(in.q_off, in.k_off, in.sel_count, in.sel_idx, N, nQ, nK, a.W, sc.keepers,
+                                          sc.k_units, a.k_per_head, sc.q_units, a.q_per_head, st);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  a.q_off = in.q_off;
+  a.k_off = in.k_off;
+  a.sel_count = in.sel_count;
+  a.sel_idx = in.sel_idx;
+  a.keepers = sc.keepers;
+  a.k_units = sc.k_units;
+  a.q_units = sc.q_units;
+  a.perm_q = in.perm_q;
+  a.perm_k = in.perm_k;
+  a.neg_lse2 = sc.neg_lse2;
+  a.neg_delta = sc.neg_delta;
+  a.k_mean = sc.k_mean;
+  a.dQ = static_cast<__nv_bfloat16*>(in.dQ);
+  a.dK = static_cast<__nv_bfloat16*>(in.dK);
+  a.dV = static_cast<__nv_bfloat16*>(in.dV);
+  a.scale = scale;
+  a.st = st;
+  a.wait_budget = wait_budget;
+  alignas(64) BwdMaps maps;
+  const void* base[4] = {in.Q, in.K, in.V, in.perm_q != nullptr ? sc.dOp : in.dO};
+  for (int t = 0; t < 4 && e == cudaSuccess; ++t)
+    for (int b = dense ? kBwdBoxes - 1 : 0; b < kBwdBoxes && e == cudaSuccess; ++b)
+      e = make_tmap_bf16_3d(&maps.m[t][b], base[t], D, N, BH, D * 2, static_cast<uint64_t>(N) * D * 2, 1u << b);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(attn_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bwd_smem<D>());
+  if (e != cudaSuccess) return e;
+  const long long units = static_cast<long long>(BH) * (a.k_per_head + a.q_per_head);
+  attn_bwd_kernel<D><<<static_cast<unsigned>(units), kBwdThreads, bwd_smem<D>(), s>>>(maps, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_bwd(const BwdInputs& in, int BH, int N, int d, int nQ, int nK, float scale,
+                            const BwdScratch& sc, DeviceStatus* st, const uint64_t* wait_budget, cudaStream_t s) {
+  return d == 128 ? launch_bwd<128>(in, BH, N, nQ, nK, scale, sc, st, wait_budget, s)
+                  : launch_bwd<64>(in, BH, N, nQ, nK, scale, sc, st, wait_budget, s);
+}
+
+}  // namespace svg2

@@ -45,6 +45,9 @@ enum : uint32_t {
   kWhereUpdate = 14,     // centroid update (debug build)
   kWherePlan = 15,       // attention work plan and range table (debug build)
   kWherePruned = 16,     // pruned assignment (debug build)
+  kWhereAttnBwdProducer = 17,
+  kWhereAttnBwdMma = 18,
+  kWhereAttnBwdSoftmax = 19,
 };
 
 constexpr int kStatusBytes = 256;
@@ -184,7 +187,67 @@ cudaError_t launch_sparse_attn(const void* Qp, const void* Kp, const void* Vp, c
                                const int32_t* k_off, const int32_t* sel_count, const int32_t* sel_idx, int BH,
                                int N, int d, int nQ, int nK, float scale, const int32_t* perm_q, void* O,
                                const AttnScratch& scratch, DeviceStatus* st, const uint64_t* wait_budget,
-                               cudaStream_t s);
+                               cudaStream_t s, float* lse = nullptr);  // lse: optional [BH, N] by permuted row
+
+// Attention gradients (svg2_attn_bwd.cu).  A unit is up to 128 rows of one cluster: rows of K (dK, dV) or
+// of Q (dQ).
+struct BwdUnit {
+  int32_t cluster;
+  int32_t row0;   // first permuted row
+  int32_t nrows;  // 1..128; 0: no unit
+};
+
+inline int bwd_max_units_per_head(int N, int n) { return N / 128 + n; }
+
+struct BwdScratch {
+  float *neg_lse2, *neg_delta;  // [BH, N] -lse log2(e) and -dO.O by permuted row
+  float* k_mean;                // [BH, d] mean of (a sample of) the plane's K rows
+  void* dOp;                    // [BH, N, d] dO in permuted order (used when perm_q is given)
+  uint32_t* keepers;            // [BH, nK, ceil(nQ / 32)] bit i: Q cluster i keeps the K cluster
+  BwdUnit *k_units, *q_units;   // [BH, bwd_max_units_per_head]
+};
+
+// nQ = 0: the dense case, which has no plan and no permutation.
+inline void carve_bwd(Carve& c, int BH, int N, int d, int nQ, int nK, BwdScratch& s) {
+  const size_t rows = static_cast<size_t>(BH) * N;
+  s.neg_lse2 = c.take<float>(rows);
+  s.neg_delta = c.take<float>(rows);
+  s.k_mean = c.take<float>(static_cast<size_t>(BH) * d);
+  s.dOp = nQ > 0 ? c.take<uint16_t>(rows * d) : nullptr;
+  s.keepers = nQ > 0 ? c.take<uint32_t>(static_cast<size_t>(BH) * nK * ((nQ + 31) / 32)) : nullptr;
+  s.k_units = nQ > 0 ? c.take<BwdUnit>(static_cast<size_t>(BH) * bwd_max_units_per_head(N, nK)) : nullptr;
+  s.q_units = nQ > 0 ? c.take<BwdUnit>(static_cast<size_t>(BH) * bwd_max_units_per_head(N, nQ)) : nullptr;
+}
+
+struct BwdInputs {
+  const void *Q, *K, *V, *O, *dO;  // Q, K, V by permuted row; O and dO by token where perm_q is given
+  const float* lse;                // by permuted row
+  const int32_t *q_off, *k_off, *sel_count, *sel_idx;  // null: dense
+  const int32_t *perm_q, *perm_k;  // optional
+  void *dQ, *dK, *dV;              // by token where the permutation is given, else by permuted row
+};
+cudaError_t launch_attn_bwd(const BwdInputs& in, int BH, int N, int d, int nQ, int nK, float scale,
+                            const BwdScratch& sc, DeviceStatus* st, const uint64_t* wait_budget, cudaStream_t s);
+
+// Layer norm (svg2_norm.cu).
+struct NormCall {
+  const void *X, *dY;          // dY: backward
+  const float *gamma, *beta;   // optional
+  float *mean, *rstd;          // [rows]: out (optional) of the forward, in of the backward
+  void* Y;                     // Y | dX
+  float *dgamma, *dbeta;       // backward, optional
+  float* partial;              // backward: [norm_max_parts][2][width]
+  long long rows;
+  int width;
+  float eps;
+};
+constexpr int kNormSms = 148;
+// At most this many CTAs (each writing one partial row of dgamma and dbeta) in the backward pass.
+inline int norm_max_parts(long long rows) {
+  const long long most = kNormSms * 8;
+  return static_cast<int>(rows < most ? rows : most);
+}
+cudaError_t launch_norm(const NormCall& n, bool f32, bool bwd, cudaStream_t s);
 
 // Dequantisation scales of the FP8 attention: one float per (b,h) plane of Q, K and V.
 struct F8Scales {

@@ -33,7 +33,9 @@ _EXPORTS = ("svg2_status_string", "svg2_workspace_size", "svg2_check_status", "s
             "svg2_dense_attn_workspace_size", "svg2_dense_attn", "svg2_driver_create", "svg2_driver_destroy",
             "svg2_driver_cache_bytes", "svg2_driver_bind_cache", "svg2_driver_reset", "svg2_driver_workspace_size",
             "svg2_driver_plan", "svg2_driver_layer", "svg2_set_wait_budget", "svg2_quantize_e4m3",
-            "svg2_sparse_attn_fp8")
+            "svg2_sparse_attn_fp8", "svg2_dense_attn_lse", "svg2_sparse_attn_lse",
+            "svg2_dense_attn_bwd_workspace_size", "svg2_dense_attn_bwd", "svg2_sparse_attn_bwd_workspace_size",
+            "svg2_sparse_attn_bwd", "svg2_layer_norm", "svg2_layer_norm_bwd_workspace_size", "svg2_layer_norm_bwd")
 
 _lib = None
 
@@ -102,6 +104,16 @@ def lib() -> ctypes.CDLL:
         L.svg2_driver_workspace_size.argtypes = [P, ctypes.POINTER(S)]
         L.svg2_driver_plan.argtypes = [P, I, I, ctypes.POINTER(I)]
         L.svg2_driver_layer.argtypes = [P, I, I, P, P, P, P, P, P, P, S, P]
+        LL = ctypes.c_longlong
+        L.svg2_dense_attn_lse.argtypes = [P, P, P, I, I, I, I, F, P, P, P, S, P]
+        L.svg2_sparse_attn_lse.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, P, S, P]
+        L.svg2_dense_attn_bwd_workspace_size.argtypes = [I, I, I, I, ctypes.POINTER(S)]
+        L.svg2_dense_attn_bwd.argtypes = [P, P, P, P, P, P, I, I, I, I, F, P, P, P, P, S, P]
+        L.svg2_sparse_attn_bwd_workspace_size.argtypes = [I, I, I, I, I, I, ctypes.POINTER(S)]
+        L.svg2_sparse_attn_bwd.argtypes = [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, F, P, P, P, P, P, P, S, P]
+        L.svg2_layer_norm.argtypes = [P, I, P, P, LL, I, F, P, P, P, P]
+        L.svg2_layer_norm_bwd_workspace_size.argtypes = [LL, I, ctypes.POINTER(S)]
+        L.svg2_layer_norm_bwd.argtypes = [P, P, I, P, P, P, LL, I, P, P, P, P, S, P]
         for name in _EXPORTS:
             if name != "svg2_status_string":
                 getattr(L, name).restype = I
@@ -384,6 +396,140 @@ def svg2_sparse_attn_noalloc(Qp: torch.Tensor, Kp: torch.Tensor, Vp: torch.Tenso
         raise ValueError("device_status: the status word takes 16 bytes")
     _check(lib().svg2_sparse_attn_noalloc(*ptr[:7], B, H, N, d, nQ, nK, float(scale), ptr[8], ptr[7],
                                           _p(device_status), _stream(stream)), "svg2_sparse_attn_noalloc")
+
+
+def _one_device(*tensors):
+    """The training calls launch on the current device's stream: every tensor must live there."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) > 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+    dev = next(iter(devices))
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def svg2_dense_attn_lse(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, O: torch.Tensor,
+                        lse: torch.Tensor, ws: torch.Tensor, stream=None):
+    """svg2_dense_attn that also writes the rows' log-sum-exp (for svg2_dense_attn_bwd)."""
+    B, H, N, d = _dims(Q, "Q")
+    n = B * H * N * d
+    _one_device(Q, K, V, O, lse, ws)
+    _check(lib().svg2_dense_attn_lse(_arg(Q, "Q", _BF16, 0), _arg(K, "K", _BF16, n), _arg(V, "V", _BF16, n), B, H, N, d,
+                                     float(scale), _arg(O, "O", _BF16, n), _arg(lse, "lse", _F32, B * H * N), _p(ws),
+                                     _nbytes(ws), _stream(stream)), "svg2_dense_attn_lse")
+
+
+def svg2_sparse_attn_lse(Qp: torch.Tensor, Kp: torch.Tensor, Vp: torch.Tensor, q_off: torch.Tensor,
+                         k_off: torch.Tensor, sel_count: torch.Tensor, sel_idx: torch.Tensor, scale: float,
+                         O: torch.Tensor, lse: torch.Tensor, ws: torch.Tensor, perm_q: Optional[torch.Tensor] = None,
+                         stream=None):
+    """svg2_sparse_attn that also writes the log-sum-exp by permuted row (for svg2_sparse_attn_bwd)."""
+    B, H, N, d, nQ, nK, ptr = _attn_args(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, O, perm_q)
+    _one_device(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, O, lse, ws, perm_q)
+    _check(lib().svg2_sparse_attn_lse(*ptr[:7], B, H, N, d, nQ, nK, float(scale), ptr[8], ptr[7],
+                                      _arg(lse, "lse", _F32, B * H * N), _p(ws), _nbytes(ws), _stream(stream)),
+           "svg2_sparse_attn_lse")
+
+
+def svg2_dense_attn_bwd_workspace_size(B: int, H: int, N: int, d: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().svg2_dense_attn_bwd_workspace_size(B, H, N, d, ctypes.byref(out)),
+           "svg2_dense_attn_bwd_workspace_size")
+    return int(out.value)
+
+
+def dense_bwd_workspace(B: int, H: int, N: int, d: int, device=None) -> torch.Tensor:
+    """A workspace tensor for svg2_dense_attn_lse and svg2_dense_attn_bwd (the status word starts at 0)."""
+    return torch.zeros(svg2_dense_attn_bwd_workspace_size(B, H, N, d), dtype=torch.uint8, device=device or "cuda")
+
+
+def svg2_dense_attn_bwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: torch.Tensor, lse: torch.Tensor,
+                        dO: torch.Tensor, scale: float, dQ: torch.Tensor, dK: torch.Tensor, dV: torch.Tensor,
+                        ws: torch.Tensor, stream=None):
+    """Gradients of dense attention from O and lse as svg2_dense_attn_lse wrote them."""
+    B, H, N, d = _dims(Q, "Q")
+    n = B * H * N * d
+    _one_device(Q, K, V, O, lse, dO, dQ, dK, dV, ws)
+    _check(lib().svg2_dense_attn_bwd(_arg(Q, "Q", _BF16, 0), _arg(K, "K", _BF16, n), _arg(V, "V", _BF16, n),
+                                     _arg(O, "O", _BF16, n), _arg(lse, "lse", _F32, B * H * N),
+                                     _arg(dO, "dO", _BF16, n), B, H, N, d, float(scale), _arg(dQ, "dQ", _BF16, n),
+                                     _arg(dK, "dK", _BF16, n), _arg(dV, "dV", _BF16, n), _p(ws), _nbytes(ws),
+                                     _stream(stream)), "svg2_dense_attn_bwd")
+
+
+def svg2_sparse_attn_bwd_workspace_size(B: int, H: int, N: int, d: int, nQ: int, nK: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().svg2_sparse_attn_bwd_workspace_size(B, H, N, d, nQ, nK, ctypes.byref(out)),
+           "svg2_sparse_attn_bwd_workspace_size")
+    return int(out.value)
+
+
+def sparse_bwd_workspace(B: int, H: int, N: int, d: int, nQ: int, nK: int, device=None) -> torch.Tensor:
+    """A workspace tensor for svg2_sparse_attn_lse and svg2_sparse_attn_bwd (the status word starts at 0)."""
+    return torch.zeros(svg2_sparse_attn_bwd_workspace_size(B, H, N, d, nQ, nK), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def svg2_sparse_attn_bwd(Qp: torch.Tensor, Kp: torch.Tensor, Vp: torch.Tensor, O: torch.Tensor, lse: torch.Tensor,
+                         dO: torch.Tensor, q_off: torch.Tensor, k_off: torch.Tensor, sel_count: torch.Tensor,
+                         sel_idx: torch.Tensor, scale: float, dQ: torch.Tensor, dK: torch.Tensor, dV: torch.Tensor,
+                         ws: torch.Tensor, perm_q: Optional[torch.Tensor] = None,
+                         perm_k: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of the sparse attention for its plan: O, dO and dQ by token when perm_q is given, dK and dV by
+    token when perm_k is."""
+    B, H, N, d, nQ, nK, ptr = _attn_args(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, O, perm_q)
+    _one_device(Qp, Kp, Vp, O, lse, dO, q_off, k_off, sel_count, sel_idx, dQ, dK, dV, ws, perm_q, perm_k)
+    BH, n = B * H, B * H * N * d
+    _check(lib().svg2_sparse_attn_bwd(*ptr[:3], ptr[7], _arg(lse, "lse", _F32, BH * N), _arg(dO, "dO", _BF16, n),
+                                      *ptr[3:7], B, H, N, d, nQ, nK, float(scale), ptr[8],
+                                      _arg(perm_k, "perm_k", _I32, BH * N, optional=True), _arg(dQ, "dQ", _BF16, n),
+                                      _arg(dK, "dK", _BF16, n), _arg(dV, "dV", _BF16, n), _p(ws), _nbytes(ws),
+                                      _stream(stream)), "svg2_sparse_attn_bwd")
+
+
+def _rows(X: torch.Tensor, name: str):
+    if X is None or X.dim() < 1:
+        raise ValueError(f"{name} must have at least one dimension")
+    width = int(X.shape[-1])
+    return (X.numel() // width if width else 0), width
+
+
+def svg2_layer_norm(X: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], eps: float,
+                    Y: torch.Tensor, mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                    stream=None):
+    """Layer norm of X [..., width] over its last dimension; mean and rstd [rows] are kept for the gradients."""
+    rows, width = _rows(X, "X")
+    _one_device(X, gamma, beta, Y, mean, rstd)
+    _check(lib().svg2_layer_norm(_arg(X, "X", _DATA, 0), _dtype(X), _arg(gamma, "gamma", _F32, width, optional=True),
+                                 _arg(beta, "beta", _F32, width, optional=True), rows, width, float(eps),
+                                 _arg(Y, "Y", (X.dtype,), rows * width), _arg(mean, "mean", _F32, rows, optional=True),
+                                 _arg(rstd, "rstd", _F32, rows, optional=True), _stream(stream)), "svg2_layer_norm")
+
+
+def svg2_layer_norm_bwd_workspace_size(rows: int, width: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().svg2_layer_norm_bwd_workspace_size(rows, width, ctypes.byref(out)),
+           "svg2_layer_norm_bwd_workspace_size")
+    return int(out.value)
+
+
+def layer_norm_bwd_workspace(rows: int, width: int, device=None) -> torch.Tensor:
+    """A workspace tensor for svg2_layer_norm_bwd (the status word starts at 0)."""
+    return torch.zeros(svg2_layer_norm_bwd_workspace_size(rows, width), dtype=torch.uint8, device=device or "cuda")
+
+
+def svg2_layer_norm_bwd(X: torch.Tensor, dY: torch.Tensor, gamma: Optional[torch.Tensor], mean: torch.Tensor,
+                        rstd: torch.Tensor, dX: torch.Tensor, dgamma: Optional[torch.Tensor],
+                        dbeta: Optional[torch.Tensor], ws: torch.Tensor, stream=None):
+    """Gradients of svg2_layer_norm from the mean and rstd it wrote."""
+    rows, width = _rows(X, "X")
+    _one_device(X, dY, gamma, mean, rstd, dX, dgamma, dbeta, ws)
+    _check(lib().svg2_layer_norm_bwd(_arg(X, "X", _DATA, 0), _arg(dY, "dY", (X.dtype,), rows * width), _dtype(X),
+                                     _arg(gamma, "gamma", _F32, width, optional=True), _arg(mean, "mean", _F32, rows),
+                                     _arg(rstd, "rstd", _F32, rows), rows, width, _arg(dX, "dX", (X.dtype,), rows * width),
+                                     _arg(dgamma, "dgamma", _F32, width, optional=True),
+                                     _arg(dbeta, "dbeta", _F32, width, optional=True), _p(ws), _nbytes(ws),
+                                     _stream(stream)), "svg2_layer_norm_bwd")
 
 
 def svg2_unpermute(Op: torch.Tensor, perm: torch.Tensor, O: torch.Tensor, stream=None):
