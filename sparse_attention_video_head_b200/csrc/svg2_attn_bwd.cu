@@ -57,6 +57,13 @@ constexpr uint32_t bwd_smem() {
          4096 + 64 /*range offsets*/ + 256 /*barriers*/;
 }
 
+// Streams of up to this many tiles hand dS over as two bf16 numbers (its rounding, and the rest) and take one
+// more product per tile; one-tile streams also take delta as sum_j P_ij dP_ij instead of from the bf16 O
+// (the key unit only when it holds every key, dense N <= 128).  Short rows average fewer rounding errors and often
+// hold like keys, and there the products are not what takes the time: over random short rows (2 to 512 keys)
+// the worst error of dQ and dK falls from 5.8e-3 and 3.0e-2 to 4.9e-3 and 2.1e-3 of their norms.
+constexpr int kBwdSplitTiles = 4;
+
 struct BwdMaps {  // [Q, K, V, dO][log2 box height], 64 columns wide, 128-byte swizzle
   CUtensorMap m[4][kBwdBoxes];
 };
@@ -275,10 +282,10 @@ struct BwdTmem {
   static constexpr uint32_t dp = 256, acc2 = 384;     // acc2: dK | dQ
 };
 
-template <int D, bool KV>
+template <int D, bool KV, bool SPLIT>
 __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, const BwdUnit un, const int bh,
                                          uint8_t* smem, BwdBars* bars, float* stats, const int32_t* r_start,
-                                         const int32_t* r_cum, const long long wb) {
+                                         const int32_t* r_cum, float* scratch, const long long wb) {
   constexpr uint32_t kTile = bwd_tile_bytes<D>();
   constexpr int kHalves = D / 64;   // 128-byte swizzle atoms across a row
   constexpr int kSteps = D / 16;    // instructions of one S or dP product
@@ -351,6 +358,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         if (!ok) break;
         tc_fence_after();
         accumulate(tmem + Tm::acc2, tmem + Tm::dp, t1 + sg * kTile, j > 0);  // dK += dS^T Q | dQ += dS K
+        if constexpr (SPLIT) accumulate(tmem + Tm::acc2, tmem + Tm::dp + 32, t1 + sg * kTile, true);
         mma_commit(smem_u32(&bars->t1_empty[sg]));
         if (more) {
           ok = wait(&bars->t2_full[ng], (j + 1) >> 1);
@@ -474,6 +482,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
     auto wait = [&](uint64_t* bar, int phase) {
       return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, st, kWhereAttnBwdSoftmax, wb));
     };
+    const bool exact_delta = SPLIT && T == 1 && (!KV || (dense && a.N <= 128));
     float2 r_sum = make_float2(0.f, 0.f);  // query unit: this half's sum of the row's rounded dS
     bool ok = true;
     for (int j = 0; j < T; ++j) {
@@ -527,29 +536,82 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       tmem_ld32p(t_dp, sv);
       tmem_ld32p(t_dp + 32, sv + 32);
       tmem_wait_ld();
-      uint32_t dk[32];
+      if (exact_delta) {
+        // delta_i = sum_j P_ij dP_ij in float32
+        if constexpr (KV) {  // over the lanes and the four warps: this CTA holds every key of the plane
+          float x[32];
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float4 d4;
-        if constexpr (KV) d4 = *reinterpret_cast<const float4*>(st_d + 2 * e);
-        else d4 = make_float4(nd_row, nd_row, nd_row, nd_row);
+          for (int i = 0; i < 32; ++i) {
+            const float2 lo = p[i >> 1], hi = p[16 + (i >> 1)];
+            const float a0 = ((i & 1) ? lo.y : lo.x) * __uint_as_float(sv[i]);
+            const float a1 = ((i & 1) ? hi.y : hi.x) * __uint_as_float(sv[32 + i]);
+            const bool up = (lane & 16) != 0;
+            x[i] = (up ? a1 : a0) + __shfl_xor_sync(0xffffffffu, up ? a0 : a1, 16);
+          }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float2 ds =
-              mul2(p[e + u], add2(make_float2(__uint_as_float(sv[2 * (e + u)]), __uint_as_float(sv[2 * (e + u) + 1])),
-                                  u == 0 ? make_float2(d4.x, d4.y) : make_float2(d4.z, d4.w)));
-          dk[e + u] = pack_bf16x2(ds.x, ds.y);
+          for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < 2 * o; ++i) {
+              const bool up = (lane & o) != 0;
+              const float keep = up ? x[i + 2 * o] : x[i];
+              x[i] = keep + __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + 2 * o], o);
+            }
+          float* red = scratch + (warp & 3) * 128 + half * 64 + 2 * lane;  // lane l ends with columns 2l, 2l + 1
+          red[0] = x[0];
+          red[1] = x[1];
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          if (half == 0) {
+            const float* c = scratch + row;
+            stats[128 + row] = -((c[0] + c[128]) + (c[256] + c[384]));
+          }
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+        } else {  // over the row's two halves
+          float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            x = fma2(p[e], make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), x);
+          stats[256 + half * 128 + row] = x.x + x.y;
+          asm volatile("bar.sync 1, 256;" ::: "memory");
+          nd_row = -(stats[256 + row] + stats[384 + row]);
         }
       }
-      tmem_st32(t_dp, dk);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {  // 32 columns at a time
+        uint32_t hi[16];
+        auto ds_pair = [&](int e) {
+          float2 d2;
+          if constexpr (KV) d2 = *reinterpret_cast<const float2*>(st_d + 32 * c + 2 * e);
+          else d2 = make_float2(nd_row, nd_row);
+          return mul2(p[16 * c + e], add2(make_float2(__uint_as_float(sv[32 * c + 2 * e]),
+                                                      __uint_as_float(sv[32 * c + 2 * e + 1])), d2));
+        };
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 ds = ds_pair(e);
+          hi[e] = pack_bf16x2(ds.x, ds.y);
+        }
+        tmem_st16(t_dp + 16 * c, hi);
+        if constexpr (!KV) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r_sum = add2(r_sum, make_float2(bf16lo_to_f32(hi[e]), bf16hi_to_f32(hi[e])));
+        }
+        if constexpr (SPLIT) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 ds = ds_pair(e);
+            hi[e] = pack_bf16x2(ds.x - bf16lo_to_f32(hi[e]), ds.y - bf16hi_to_f32(hi[e]));
+          }
+          tmem_st16(t_dp + 32 + 16 * c, hi);
+          if constexpr (!KV) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r_sum = add2(r_sum, make_float2(bf16lo_to_f32(hi[e]), bf16hi_to_f32(hi[e])));
+          }
+        }
+      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
-      if constexpr (!KV) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) r_sum = add2(r_sum, make_float2(bf16lo_to_f32(dk[e]), bf16hi_to_f32(dk[e])));
-      }
     }
     float r_row = 0.f;
     if constexpr (!KV) {  // both halves' sums (the streamed lse buffer is free in a query unit)
@@ -717,8 +779,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after();
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwdOtherRegs) : "memory");
   else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwdSoftmaxRegs) : "memory");
-  if (kv) bwd_unit<D, true>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, wb);
-  else bwd_unit<D, false>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, wb);
+  float* scratch = reinterpret_cast<float*>(r_start);
+  const bool split = bars->L <= kBwdSplitTiles * 128;
+  if (kv) {
+    if (split) bwd_unit<D, true, true>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, scratch, wb);
+    else bwd_unit<D, true, false>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, scratch, wb);
+  } else {
+    if (split) bwd_unit<D, false, true>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, scratch, wb);
+    else bwd_unit<D, false, false>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, scratch, wb);
+  }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
