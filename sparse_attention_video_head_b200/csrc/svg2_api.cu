@@ -497,12 +497,11 @@ int svg2_sparse_attn_fp8(const void* Qp8, const void* Kp8, const void* Vp8, cons
 namespace {
 struct DenseCarve {
   DeviceStatus* st;
-  int32_t *q_off, *k_off, *sel_count, *sel_idx;
+  int32_t *k_off, *sel_count, *sel_idx;
   AttnScratch attn;
 };
 void carve_dense(Carve& c, int BH, int N, DenseCarve& D) {
   D.st = c.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
-  D.q_off = c.take<int32_t>(static_cast<size_t>(BH) * 2);
   D.k_off = c.take<int32_t>(static_cast<size_t>(BH) * 2);
   D.sel_count = c.take<int32_t>(BH);
   D.sel_idx = c.take<int32_t>(BH);
@@ -535,11 +534,8 @@ static int dense_attn_call(const void* Q, const void* K, const void* V, int B, i
   r = check_ws(ws, ws_bytes, c.off);
   if (r != SVG2_OK) return r;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_dense_plan(BH, N, D.q_off, D.k_off, D.sel_count, D.sel_idx, s);
-  if (e == cudaSuccess)
-    e = launch_sparse_attn(Q, K, V, D.q_off, D.k_off, D.sel_count, D.sel_idx, BH, N, d, 1, 1, scale, nullptr, O,
-                           D.attn, D.st, wait_budget_of(D.st), s, lse);
-  return to_status(e);
+  return to_status(launch_dense_attn(Q, K, V, BH, N, d, scale, O, lse, D.k_off, D.sel_count, D.sel_idx, D.attn, D.st,
+                                     wait_budget_of(D.st), s));
 }
 
 int svg2_dense_attn(const void* Q, const void* K, const void* V, int B, int H, int N, int d, float scale, void* O,

@@ -54,7 +54,7 @@ constexpr uint32_t bwd_tile_bytes() { return 128u * D * 2u; }
 template <int D>
 constexpr uint32_t bwd_smem() {
   return 6 * bwd_tile_bytes<D>() + 1024 /*align*/ + 4 * 512 /*lse, delta of two stages*/ + 4096 /*range starts*/ +
-         4096 + 64 /*range offsets*/ + 256 /*barriers*/;
+         4096 + 64 /*range offsets*/ + 2048 /*range segments*/ + 256 /*barriers*/;
 }
 
 // Streams of up to this many tiles hand dS over as two bf16 numbers (its rounding, and the rest) and take one
@@ -69,14 +69,14 @@ struct BwdMaps {  // [Q, K, V, dO][log2 box height], 64 columns wide, 128-byte s
 };
 
 struct BwdArgs {
-  const int32_t *q_off, *k_off, *sel_count, *sel_idx;  // null: dense
-  const uint32_t* keepers;                             // [BH, nK, W] bit i: Q cluster i keeps this K cluster
+  const int32_t *q_off, *k_off;     // null: dense
+  const uint32_t *keepers, *kept;   // the selection as bits, by K cluster and by Q cluster
   const BwdUnit *k_units, *q_units;                    // [BH, per_head]
   const int32_t *perm_q, *perm_k;
   const float *neg_lse2, *neg_delta;                   // [BH, N] -lse log2(e), -delta, by permuted row
   const float* k_mean;                                 // [BH, D]
   __nv_bfloat16 *dQ, *dK, *dV;
-  int BH, N, nQ, nK, W, k_per_head, q_per_head;
+  int BH, N, nQ, nK, k_per_head, q_per_head;
   float scale;
   DeviceStatus* st;
   const uint64_t* wait_budget;
@@ -89,14 +89,6 @@ struct BwdBars {
   int32_t L, nranges;
 };
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<unsigned long long&>(d))
-      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
-  return d;
-}
-
 // 4-byte asynchronous copy; bytes = 0 writes a zero and reads nothing.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -104,8 +96,8 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_
 
 // ------------------------------------------------------------------------------------------------
 // delta_i = dO_i . O_i and the scaled log-sum-exp, by permuted row; with perm, dO's rows in permuted
-// order too.  D / 8 lanes per row, 16 bytes each: bound by the reads of O and dO.  The CTAs past row_ctas
-// take the mean of up to kMeanRows evenly spaced K rows of one plane each.
+// order too.  D / 8 lanes per row, 16 bytes each: bound by the reads of O and dO.  The first BH CTAs take
+// the mean of up to kMeanRows evenly spaced K rows of one plane each.
 // ------------------------------------------------------------------------------------------------
 constexpr int kMeanRows = 512;
 
@@ -116,7 +108,7 @@ __device__ void mean_key(const uint4* __restrict__ K, int bh, int N, float* __re
   const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
   const int S = min(N, kMeanRows);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 16
   for (int t = group; t < S; t += kGroups) {
     const long long row = static_cast<long long>(bh) * N + static_cast<long long>(t) * N / S;
     const uint4 w = __ldg(K + row * kLanes + sub);
@@ -139,17 +131,17 @@ template <int D>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__ O, const uint4* __restrict__ dO,
                                                        const float* __restrict__ lse, const int32_t* __restrict__ perm,
                                                        const uint4* __restrict__ K, int N, long long rows,
-                                                       int row_ctas, float* __restrict__ neg_lse2,
+                                                       int BH, float* __restrict__ neg_lse2,
                                                        float* __restrict__ neg_delta, uint4* __restrict__ dOp,
                                                        float* __restrict__ k_mean, DeviceStatus* st) {
-  if (static_cast<int>(blockIdx.x) >= row_ctas) {
-    mean_key<D>(K, blockIdx.x - row_ctas, N, k_mean);
+  if (static_cast<int>(blockIdx.x) < BH) {
+    mean_key<D>(K, blockIdx.x, N, k_mean);
     return;
   }
   constexpr int kLanes = D / 8;
   const int sub = threadIdx.x % kLanes;
-  const long long step = static_cast<long long>(row_ctas) * (256 / kLanes);
-  const long long first = static_cast<long long>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes;
+  const long long step = static_cast<long long>(gridDim.x - BH) * (256 / kLanes);
+  const long long first = static_cast<long long>(blockIdx.x - BH) * (256 / kLanes) + threadIdx.x / kLanes;
   // every lane of a warp takes part in the shuffles: rows past the end only skip their memory
   for (long long r0 = first - (threadIdx.x % 32) / kLanes; r0 < rows; r0 += step) {
     const long long r = r0 + (threadIdx.x % 32) / kLanes;
@@ -189,46 +181,58 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
 }
 
 // ------------------------------------------------------------------------------------------------
-// The sparse plan, one CTA per (b,h): which Q clusters keep each K cluster (the transposed selection,
-// as bits), and the units of both kinds.  A K cluster listed twice for one Q cluster, or an index out
-// of range, latches SVG2_ERR_DEVICE_BOUNDS: the gradient kernel then does nothing.
+// The sparse plan, one CTA per (b,h): the selection as bits both ways, and the units of both kinds.  A K
+// cluster listed twice for one Q cluster, or an index out of range, latches SVG2_ERR_DEVICE_BOUNDS: the
+// gradient kernel then does nothing.
+//
+// A unit costs as many tiles as its stream is long, however few of its 128 rows are used, and clusters
+// rarely end on a multiple of 128.  So what is left of a cluster after its full tiles shares a unit with the
+// rows that follow whenever that saves the next cluster a unit: the joint stream is the union of the
+// clusters' streams, never longer than the two, and the pairs that a row's own cluster does not keep are masked.
+// On 8 heads of 12480 tokens in 64 / 256 clusters (49 rows per K cluster) at 60 % kept, ... .
 // ------------------------------------------------------------------------------------------------
-__device__ void write_units(const int32_t* off, int n, int N, int per_head, BwdUnit* out, int32_t* count,
+constexpr int kBwdMaxSegments = 16;
+
+__device__ void write_units(const int32_t* off, int n, int N, int per_head, BwdUnit* out, int32_t* smem_off,
                             DeviceStatus* st) {
-  // count[i] = exclusive prefix of the clusters' 128-row units
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int r0 = off[i], len = off[i + 1] - r0;
-    const bool ok = r0 >= 0 && len > 0 && r0 <= N - len;
-    SVG2_DEBUG_CHECK(ok || len == 0, st, kWherePlan, i, r0);
-    count[i] = ok ? (len + 127) / 128 : 0;
-  }
+  __shared__ int32_t total;
+  for (int i = threadIdx.x; i <= n; i += blockDim.x) smem_off[i] = off[i];
   __syncthreads();
-  if (threadIdx.x < 32) {
-    int run = 0;
-    for (int b = 0; b < n; b += 32) {
-      const int i = b + threadIdx.x;
-      const int v = i < n ? count[i] : 0;
-      int incl = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, incl, o);
-        if (static_cast<int>(threadIdx.x) >= o) incl += u;
+  if (threadIdx.x == 0) {
+    int count = 0;
+    BwdUnit open{0, 0, 0, 0};  // a unit that can still take rows
+    auto emit = [&](const BwdUnit& u) {
+      if (count < per_head) out[count] = u;
+      ++count;
+    };
+    int end = smem_off[0];
+    for (int j = 0; j < n; ++j) {
+      const int start0 = end;
+      end = smem_off[j + 1];
+      int start = start0, left = end - start0;
+      const bool ok = start >= 0 && left > 0 && start <= N - left;
+      SVG2_DEBUG_CHECK(ok || left == 0, st, kWherePlan, j, start);
+      if (!ok) continue;
+      if (open.nrows > 0 && open.row0 + open.nrows == start && j - open.cluster < kBwdMaxSegments) {
+        const int t = min(128 - open.nrows, left);
+        if ((left - t + 127) / 128 < (left + 127) / 128) {
+          open.nrows += t;
+          open.nseg = j - open.cluster + 1;
+          start += t;
+          left -= t;
+        }
       }
-      if (i < n) count[i] = run + incl - v;
-      run += __shfl_sync(0xffffffffu, incl, 31);
+      if (left > 0) {
+        if (open.nrows > 0) emit(open);
+        for (; left >= 128; start += 128, left -= 128) emit(BwdUnit{j, start, 128, 1});
+        open = BwdUnit{j, start, left, 1};
+      }
     }
-    if (threadIdx.x == 0) count[n] = run;
+    if (open.nrows > 0) emit(open);
+    total = count;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const int r0 = off[i], len = off[i + 1] - r0;
-    const int units = count[i + 1] - count[i];
-    for (int u = 0; u < units; ++u) {
-      const int slot = count[i] + u;
-      if (slot < per_head) out[slot] = BwdUnit{i, r0 + u * 128, min(128, len - u * 128)};
-    }
-  }
-  for (int s = count[n] + threadIdx.x; s < per_head; s += blockDim.x) out[s] = BwdUnit{0, 0, 0};
+  for (int s = total + threadIdx.x; s < per_head; s += blockDim.x) out[s] = BwdUnit{0, 0, 0, 0};
   __syncthreads();
 }
 
@@ -236,36 +240,45 @@ __global__ void __launch_bounds__(512) bwd_plan_kernel(const int32_t* __restrict
                                                        const int32_t* __restrict__ k_off,
                                                        const int32_t* __restrict__ sel_count,
                                                        const int32_t* __restrict__ sel_idx, int N, int nQ, int nK,
-                                                       int W, uint32_t* __restrict__ keepers,
+                                                       uint32_t* __restrict__ keepers, uint32_t* __restrict__ kept,
                                                        BwdUnit* __restrict__ k_units, int k_per_head,
                                                        BwdUnit* __restrict__ q_units, int q_per_head,
                                                        DeviceStatus* st) {
-  extern __shared__ uint32_t bits[];  // [nK, W]
-  __shared__ int32_t count[kMaxClustersAssign + 1];
+  extern __shared__ uint32_t bits[];  // [nK, WQ], then [16 warps][WK]
+  __shared__ int32_t offsets[kMaxClustersAssign + 1];
+  const int WQ = (nQ + 31) / 32, WK = (nK + 31) / 32;
   const int bh = blockIdx.x;
-  for (int w = threadIdx.x; w < nK * W; w += blockDim.x) bits[w] = 0u;
+  for (int w = threadIdx.x; w < nK * WQ; w += blockDim.x) bits[w] = 0u;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* mine = bits + nK * WQ + warp * WK;
   for (int i = warp; i < nQ; i += static_cast<int>(blockDim.x >> 5)) {
     const size_t row = static_cast<size_t>(bh) * nQ + i;
-    const int cnt = sel_count[row];
+    for (int w = lane; w < WK; w += 32) mine[w] = 0u;
+    __syncwarp();
+    int cnt = sel_count[row];
     if (cnt < 0 || cnt > nK) {
       if (lane == 0) raise_status(st, kStatusDeviceBounds, kWherePlan, i, cnt);
-      continue;
+      cnt = 0;
     }
     for (int e = lane; e < cnt; e += 32) {
       const int j = sel_idx[row * nK + e];
       const uint32_t bit = 1u << (i & 31);
-      if (j < 0 || j >= nK || (atomicOr(&bits[j * W + (i >> 5)], bit) & bit) != 0u)
+      if (j < 0 || j >= nK || (atomicOr(&bits[j * WQ + (i >> 5)], bit) & bit) != 0u)
         raise_status(st, kStatusDeviceBounds, kWherePlan, i, j);
+      else
+        atomicOr(&mine[j >> 5], 1u << (j & 31));
     }
+    __syncwarp();
+    for (int w = lane; w < WK; w += 32) kept[row * WK + w] = mine[w];
+    __syncwarp();
   }
   __syncthreads();
-  for (int w = threadIdx.x; w < nK * W; w += blockDim.x) keepers[static_cast<size_t>(bh) * nK * W + w] = bits[w];
+  for (int w = threadIdx.x; w < nK * WQ; w += blockDim.x) keepers[static_cast<size_t>(bh) * nK * WQ + w] = bits[w];
   write_units(k_off + static_cast<size_t>(bh) * (nK + 1), nK, N, k_per_head,
-              k_units + static_cast<size_t>(bh) * k_per_head, count, st);
+              k_units + static_cast<size_t>(bh) * k_per_head, offsets, st);
   write_units(q_off + static_cast<size_t>(bh) * (nQ + 1), nQ, N, q_per_head,
-              q_units + static_cast<size_t>(bh) * q_per_head, count, st);
+              q_units + static_cast<size_t>(bh) * q_per_head, offsets, st);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -282,10 +295,10 @@ struct BwdTmem {
   static constexpr uint32_t dp = 256, acc2 = 384;     // acc2: dK | dQ
 };
 
-template <int D, bool KV, bool SPLIT>
+template <int D, bool KV, bool SPLIT, bool MULTI>
 __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, const BwdUnit un, const int bh,
                                          uint8_t* smem, BwdBars* bars, float* stats, const int32_t* r_start,
-                                         const int32_t* r_cum, float* scratch, const long long wb) {
+                                         const int32_t* r_cum, const uint16_t* r_seg, float* scratch, const long long wb) {
   constexpr uint32_t kTile = bwd_tile_bytes<D>();
   constexpr int kHalves = D / 64;   // 128-byte swizzle atoms across a row
   constexpr int kSteps = D / 16;    // instructions of one S or dP product
@@ -294,7 +307,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
   const uint32_t tmem = bars->tmem_base;
   const int L = bars->L;
   const int T = (L + 127) / 128;
-  const bool dense = a.sel_idx == nullptr;
+  const bool dense = a.q_off == nullptr;
   DeviceStatus* st = a.st;
   const uint32_t r1 = smem_u32(smem), r2 = r1 + kTile, t1 = r1 + 2 * kTile, t2 = r1 + 4 * kTile;
 
@@ -479,6 +492,12 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       nl_row = a.neg_lse2[plane + un.row0 + row];
       nd_row = a.neg_delta[plane + un.row0 + row];
     }
+    // MULTI: this row's cluster among the unit's, and the range that holds this half's first column
+    int seg = 0, range = 0;
+    if constexpr (MULTI) {
+      const int32_t* off = KV ? a.k_off + static_cast<size_t>(bh) * (a.nK + 1) : a.q_off + static_cast<size_t>(bh) * (a.nQ + 1);
+      while (seg + 1 < un.nseg && off[un.cluster + seg + 1] <= un.row0 + row) ++seg;
+    }
     auto wait = [&](uint64_t* bar, int phase) {
       return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, st, kWhereAttnBwdSoftmax, wb));
     };
@@ -504,6 +523,22 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
 #pragma unroll
         for (int e = 0; e < 64; ++e)
           if (e >= valid) sv[e] = __float_as_uint(-INFINITY);
+      }
+      if constexpr (MULTI) {  // pairs that this row's cluster does not keep: P = 0
+        const int p0 = j * 128 + half * 64;
+        unsigned long long drop = 0ull;
+        if (p0 < L) {
+          while (r_cum[range + 1] <= p0) ++range;
+          for (int e = range, at = 0; at < 64 && p0 + at < L; ++e) {
+            const int n = min(r_cum[e + 1] - (p0 + at), 64 - at);
+            if (!((r_seg[e] >> seg) & 1)) drop |= (n == 64 ? ~0ull : (1ull << n) - 1ull) << at;
+            at += n;
+          }
+        }
+        const uint32_t d0 = static_cast<uint32_t>(drop), d1 = static_cast<uint32_t>(drop >> 32);
+#pragma unroll
+        for (int e = 0; e < 64; ++e)
+          if (((e < 32 ? d0 : d1) >> (e & 31)) & 1u) sv[e] = __float_as_uint(-INFINITY);
       }
       // P = 2^(s log2(e) - lse log2(e))
       float2 p[32];
@@ -673,29 +708,26 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
   }
 }
 
-// The ranges of plane rows that a unit's stream is made of (warp 9): start rows and the exclusive
-// prefix of their lengths.
+// The ranges of plane rows that a unit's stream is made of (warp 9): the clusters kept by any of the
+// unit's, their start rows, the exclusive prefix of their lengths and which of the unit's clusters keep them.
 __device__ __forceinline__ void build_ranges(const BwdArgs& a, const BwdUnit un, int bh, bool kv, int32_t* r_start,
-                                             int32_t* r_cum, BwdBars* bars) {
+                                             int32_t* r_cum, uint16_t* r_seg, BwdBars* bars) {
   const int lane = threadIdx.x & 31;
-  const int32_t* off = kv ? a.q_off + static_cast<size_t>(bh) * (a.nQ + 1) : a.k_off + static_cast<size_t>(bh) * (a.nK + 1);
-  int cnt = 0;
-  if (kv) {  // the set bits of this K cluster's row
-    uint32_t w = lane < a.W ? a.keepers[(static_cast<size_t>(bh) * a.nK + un.cluster) * a.W + lane] : 0u;
-    const int mine = __popc(w);
-    int incl = mine;
+  const int rows = kv ? a.nK : a.nQ, cols = kv ? a.nQ : a.nK, W = (cols + 31) / 32;
+  const uint32_t* bits = (kv ? a.keepers : a.kept) + (static_cast<size_t>(bh) * rows + un.cluster) * W;
+  const int32_t* off = (kv ? a.q_off : a.k_off) + static_cast<size_t>(bh) * (cols + 1);
+  uint32_t any = 0u;
+  if (lane < W)
+    for (int s = 0; s < un.nseg; ++s) any |= bits[s * W + lane];
+  const int mine = __popc(any);
+  int incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    cnt = __shfl_sync(0xffffffffu, incl, 31);
-    for (int e = incl - mine; w != 0u; ++e, w &= w - 1) r_start[e] = lane * 32 + __ffs(w) - 1;
-  } else {
-    const size_t row = static_cast<size_t>(bh) * a.nQ + un.cluster;
-    cnt = a.sel_count[row];  // the plan kernel has checked the count and the indices
-    for (int e = lane; e < cnt; e += 32) r_start[e] = a.sel_idx[row * a.nK + e];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
   }
+  const int cnt = __shfl_sync(0xffffffffu, incl, 31);
+  for (int e = incl - mine; any != 0u; ++e, any &= any - 1) r_start[e] = lane * 32 + __ffs(any) - 1;
   __syncwarp();
   int run = 0;
   for (int b = 0; b < cnt; b += 32) {
@@ -705,18 +737,21 @@ __device__ __forceinline__ void build_ranges(const BwdArgs& a, const BwdUnit un,
       s0 = off[i];
       len = off[i + 1] - s0;
       if (s0 < 0 || len < 0 || s0 > a.N - len) s0 = len = 0;  // malformed offsets hold no rows
+      uint32_t seg = 0u;
+      for (int s = 0; s < un.nseg; ++s) seg |= ((bits[s * W + (i >> 5)] >> (i & 31)) & 1u) << s;
+      r_seg[b + lane] = static_cast<uint16_t>(seg);
     }
-    int incl = len;
+    int sum = len;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
     }
     if (b + lane < cnt) {
       r_start[b + lane] = s0;
-      r_cum[b + lane] = run + incl - len;
+      r_cum[b + lane] = run + sum - len;
     }
-    run += __shfl_sync(0xffffffffu, incl, 31);
+    run += __shfl_sync(0xffffffffu, sum, 31);
   }
   if (lane == 0) {
     r_cum[cnt] = run;
@@ -724,7 +759,11 @@ __device__ __forceinline__ void build_ranges(const BwdArgs& a, const BwdUnit un,
   }
 }
 
-template <int D>
+// Dense attention with long and with short streams, and the sparse plan, are kernels of their own: each holds
+// only the unit variants that it can meet, which keeps the hot loops' registers free of spills.
+enum class BwdKind { kDense, kDenseShort, kSparse };
+
+template <int D, BwdKind KIND>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs a) {
   if (__syncthreads_or(status_set(a.st))) return;  // the whole CTA, or none of it
@@ -734,9 +773,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const int idx = kv ? blockIdx.x : blockIdx.x - nk;
   const int per = kv ? a.k_per_head : a.q_per_head;
   const int bh = idx / per, u = idx % per;
-  const bool dense = a.sel_idx == nullptr;
+  constexpr bool dense = KIND != BwdKind::kSparse;
   BwdUnit un;
-  if (dense) un = BwdUnit{0, u * 128, min(128, a.N - u * 128)};
+  if (dense) un = BwdUnit{0, u * 128, min(128, a.N - u * 128), 1};
   else un = (kv ? a.k_units : a.q_units)[idx];
   if (un.nrows <= 0) return;
   const long long wb = effective_wait_budget(a.wait_budget);
@@ -747,7 +786,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   float* stats = reinterpret_cast<float*>(smem + 6 * kTile);  // [stage][lse | delta][128]
   int32_t* r_start = reinterpret_cast<int32_t*>(stats + 512);
   int32_t* r_cum = r_start + kBwdMaxRanges;  // kBwdMaxRanges + 1 entries
-  BwdBars* bars = reinterpret_cast<BwdBars*>(r_cum + kBwdMaxRanges + 16);
+  uint16_t* r_seg = reinterpret_cast<uint16_t*>(r_cum + kBwdMaxRanges + 16);
+  BwdBars* bars = reinterpret_cast<BwdBars*>(r_seg + kBwdMaxRanges);
   const int warp = threadIdx.x >> 5;
 
   if (threadIdx.x == 0) {
@@ -771,7 +811,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_relinquish();
   }
   if (warp == kBwdProducerWarp) {
-    if (!dense) build_ranges(a, un, bh, kv, r_start, r_cum, bars);
+    if (!dense) build_ranges(a, un, bh, kv, r_start, r_cum, r_seg, bars);
     else if ((threadIdx.x & 31) == 0) bars->L = a.N;
   }
   tc_fence_before();
@@ -780,14 +820,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBwdOtherRegs) : "memory");
   else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwdSoftmaxRegs) : "memory");
   float* scratch = reinterpret_cast<float*>(r_start);
-  const bool split = bars->L <= kBwdSplitTiles * 128;
-  if (kv) {
-    if (split) bwd_unit<D, true, true>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, scratch, wb);
-    else bwd_unit<D, true, false>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, scratch, wb);
+#define SVG2_BWD_UNIT(KV, SPLIT, MULTI) \
+  bwd_unit<D, KV, SPLIT, MULTI>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, r_seg, scratch, wb)
+  if constexpr (dense) {
+    constexpr bool kShort = KIND == BwdKind::kDenseShort;
+    if (kv) SVG2_BWD_UNIT(true, kShort, false);
+    else SVG2_BWD_UNIT(false, kShort, false);
   } else {
-    if (split) bwd_unit<D, false, true>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, scratch, wb);
-    else bwd_unit<D, false, false>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, scratch, wb);
+    const bool split = bars->L <= kBwdSplitTiles * 128, multi = un.nseg > 1;
+    if (kv) {
+      if (split) SVG2_BWD_UNIT(true, true, true);  // (with one cluster its mask drops nothing)
+      else if (multi) SVG2_BWD_UNIT(true, false, true);
+      else SVG2_BWD_UNIT(true, false, false);
+    } else {
+      if (split) SVG2_BWD_UNIT(false, true, true);
+      else if (multi) SVG2_BWD_UNIT(false, false, true);
+      else SVG2_BWD_UNIT(false, false, false);
+    }
   }
+#undef SVG2_BWD_UNIT
   __syncwarp();
   tc_fence_before();
   __syncthreads();
@@ -806,7 +857,7 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   const unsigned grid = static_cast<unsigned>(rows / kRows + 1 < 148 * 16 ? rows / kRows + 1 : 148 * 16);
   bwd_prep_kernel<D><<<grid + BH, 256, 0, s>>>(static_cast<const uint4*>(in.O), static_cast<const uint4*>(in.dO),
                                                in.lse, in.perm_q, static_cast<const uint4*>(in.K), N, rows,
-                                               static_cast<int>(grid), sc.neg_lse2, sc.neg_delta,
+                                               BH, sc.neg_lse2, sc.neg_delta,
                                                in.perm_q != nullptr ? static_cast<uint4*>(sc.dOp) : nullptr,
                                                sc.k_mean, st);
   cudaError_t e = cudaGetLastError();
@@ -816,23 +867,21 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   a.N = N;
   a.nQ = nQ;
   a.nK = nK;
-  a.W = (nQ + 31) / 32;
   a.k_per_head = dense ? (N + 127) / 128 : bwd_max_units_per_head(N, nK);
   a.q_per_head = dense ? (N + 127) / 128 : bwd_max_units_per_head(N, nQ);
   if (!dense) {
-    const uint32_t bits = static_cast<uint32_t>(nK) * a.W * 4;
-    e = cudaFuncSetAttribute(bwd_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 131072);
+    const uint32_t bits = (static_cast<uint32_t>(nK) * ((nQ + 31) / 32) + 16u * ((nK + 31) / 32)) * 4;
+    e = cudaFuncSetAttribute(bwd_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 131072 + 2048);
     if (e != cudaSuccess) return e;
-    bwd_plan_kernel<<<BH, 512, bits, s>>>(in.q_off, in.k_off, in.sel_count, in.sel_idx, N, nQ, nK, a.W, sc.keepers,
-                                          sc.k_units, a.k_per_head, sc.q_units, a.q_per_head, st);
+    bwd_plan_kernel<<<BH, 512, bits, s>>>(in.q_off, in.k_off, in.sel_count, in.sel_idx, N, nQ, nK, sc.keepers,
+                                          sc.kept, sc.k_units, a.k_per_head, sc.q_units, a.q_per_head, st);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   a.q_off = in.q_off;
   a.k_off = in.k_off;
-  a.sel_count = in.sel_count;
-  a.sel_idx = in.sel_idx;
   a.keepers = sc.keepers;
+  a.kept = sc.kept;
   a.k_units = sc.k_units;
   a.q_units = sc.q_units;
   a.perm_q = in.perm_q;
@@ -852,10 +901,13 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
     for (int b = dense ? kBwdBoxes - 1 : 0; b < kBwdBoxes && e == cudaSuccess; ++b)
       e = make_tmap_bf16_3d(&maps.m[t][b], base[t], D, N, BH, D * 2, static_cast<uint64_t>(N) * D * 2, 1u << b);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(attn_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, bwd_smem<D>());
+  auto* kernel = !dense ? attn_bwd_kernel<D, BwdKind::kSparse>
+                        : (N <= kBwdSplitTiles * 128 ? attn_bwd_kernel<D, BwdKind::kDenseShort>
+                                                     : attn_bwd_kernel<D, BwdKind::kDense>);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bwd_smem<D>());
   if (e != cudaSuccess) return e;
   const long long units = static_cast<long long>(BH) * (a.k_per_head + a.q_per_head);
-  attn_bwd_kernel<D><<<static_cast<unsigned>(units), kBwdThreads, bwd_smem<D>(), s>>>(maps, a);
+  kernel<<<static_cast<unsigned>(units), kBwdThreads, bwd_smem<D>(), s>>>(maps, a);
   return cudaGetLastError();
 }
 

@@ -336,6 +336,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<const unsigned long long&>(a)), "l"(reinterpret_cast<const unsigned long long&>(b)));
+  return d;
+}
+
 // 2^x for a pair of floats on the FMA and ALU pipes instead of the MUFU.  x = n + f with n the
 // nearest integer (the rounding of x + 1.5 * 2^23 puts it in the low mantissa bits) and f in
 // [-1/2, 1/2]; 2^f is the cubic of least maximum relative error on that interval (fitted here by
@@ -418,6 +426,10 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The same copy, or 16 zero bytes (src is not read) when `in` is false.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16u : 0u) : "memory");
 }
 // Arrive on `bar` once every cp.async this thread has issued so far has landed (the barrier's
 // expected count includes this arrival: .noinc).

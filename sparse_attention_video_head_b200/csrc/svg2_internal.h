@@ -189,12 +189,13 @@ cudaError_t launch_sparse_attn(const void* Qp, const void* Kp, const void* Vp, c
                                const AttnScratch& scratch, DeviceStatus* st, const uint64_t* wait_budget,
                                cudaStream_t s, float* lse = nullptr);  // lse: optional [BH, N] by permuted row
 
-// Attention gradients (svg2_attn_bwd.cu).  A unit is up to 128 rows of one cluster: rows of K (dK, dV) or
-// of Q (dQ).
+// Attention gradients (svg2_attn_bwd.cu).  A unit is up to 128 consecutive permuted rows of K (dK, dV) or of
+// Q (dQ), in one cluster or in several.
 struct BwdUnit {
-  int32_t cluster;
-  int32_t row0;   // first permuted row
-  int32_t nrows;  // 1..128; 0: no unit
+  int32_t cluster;  // the first row's
+  int32_t row0;     // first permuted row
+  int32_t nrows;    // 1..128; 0: no unit
+  int32_t nseg;     // clusters from the first row's to the last row's (empty ones counted), at most 16
 };
 
 inline int bwd_max_units_per_head(int N, int n) { return N / 128 + n; }
@@ -204,6 +205,7 @@ struct BwdScratch {
   float* k_mean;                // [BH, d] mean of (a sample of) the plane's K rows
   void* dOp;                    // [BH, N, d] dO in permuted order (used when perm_q is given)
   uint32_t* keepers;            // [BH, nK, ceil(nQ / 32)] bit i: Q cluster i keeps the K cluster
+  uint32_t* kept;               // [BH, nQ, ceil(nK / 32)] bit j: the Q cluster keeps K cluster j
   BwdUnit *k_units, *q_units;   // [BH, bwd_max_units_per_head]
 };
 
@@ -215,6 +217,7 @@ inline void carve_bwd(Carve& c, int BH, int N, int d, int nQ, int nK, BwdScratch
   s.k_mean = c.take<float>(static_cast<size_t>(BH) * d);
   s.dOp = nQ > 0 ? c.take<uint16_t>(rows * d) : nullptr;
   s.keepers = nQ > 0 ? c.take<uint32_t>(static_cast<size_t>(BH) * nK * ((nQ + 31) / 32)) : nullptr;
+  s.kept = nQ > 0 ? c.take<uint32_t>(static_cast<size_t>(BH) * nQ * ((nK + 31) / 32)) : nullptr;
   s.k_units = nQ > 0 ? c.take<BwdUnit>(static_cast<size_t>(BH) * bwd_max_units_per_head(N, nK)) : nullptr;
   s.q_units = nQ > 0 ? c.take<BwdUnit>(static_cast<size_t>(BH) * bwd_max_units_per_head(N, nQ)) : nullptr;
 }
@@ -241,10 +244,10 @@ struct NormCall {
   int width;
   float eps;
 };
-constexpr int kNormSms = 148;
+constexpr int kNormSms = 148, kNormMaxPerSm = 8;
 // At most this many CTAs (each writing one partial row of dgamma and dbeta) in the backward pass.
 inline int norm_max_parts(long long rows) {
-  const long long most = kNormSms * 8;
+  const long long most = kNormSms * kNormMaxPerSm;
   return static_cast<int>(rows < most ? rows : most);
 }
 cudaError_t launch_norm(const NormCall& n, bool f32, bool bwd, cudaStream_t s);
@@ -271,8 +274,10 @@ cudaError_t launch_gather_e4m3(const void* X0, const void* X1, bool f32, const i
                                const uint32_t* amax0, const uint32_t* amax1, void* Y0, void* Y1, cudaStream_t s,
                                DeviceStatus* st);
 cudaError_t launch_amax_to_scale(uint32_t* amax, int n, cudaStream_t s);
-cudaError_t launch_dense_plan(int BH, int N, int32_t* q_off, int32_t* k_off, int32_t* sel_count, int32_t* sel_idx,
-                              cudaStream_t s);
+// Dense attention: one cluster per head (k_off [BH, 2], sel_count and sel_idx [BH] are scratch).
+cudaError_t launch_dense_attn(const void* Q, const void* K, const void* V, int BH, int N, int d, float scale, void* O,
+                              float* lse, int32_t* k_off, int32_t* sel_count, int32_t* sel_idx, const AttnScratch& sc,
+                              DeviceStatus* st, const uint64_t* wait_budget, cudaStream_t s);
 
 cudaError_t launch_selftest_mma(const void* A, const void* Bm, int n, const void* V, float* C, float* O,
                                 DeviceStatus* st, cudaStream_t s);

@@ -2,13 +2,20 @@
 //   mean = sum x / W,  rstd = (sum (x - mean)^2 / W + eps)^(-1/2),  xhat = (x - mean) rstd,  y = xhat gamma + beta
 //   g = dY gamma,  dX = rstd (g - sum g / W - xhat (sum g xhat) / W),  dgamma = sum_rows dY xhat,  dbeta = sum_rows dY
 // Bound by memory: the forward reads X and writes Y once, the backward reads X and dY and writes dX once, with
-// each row held in registers between (so the variance is taken over x - mean, not as a difference of
-// squares).  A row belongs to a group of threads: 8, 16 or 32 lanes of a warp when it is short, a CTA when
-// it is long; thread t of a group holds the same columns of every row it meets, so gamma's and beta's
-// gradients are summed in registers over the rows, then over the CTA's groups in shared memory, and one
-// partial row per CTA goes to the workspace; a second kernel adds the partial rows in a fixed order.  No
-// atomics: the same bits on every run.
+// each row held in registers between (so the variance is taken over x - mean, not as a difference of squares).
+//
+// A row belongs to a group of threads: 8, 16 or 32 lanes of a warp when it is short, a CTA when it is long.
+// Every thread copies its own 16-byte vectors of the next rows into its own slots of a shared-memory ring
+// (cp.async) while it works on the current one, so reads stay in flight through the row sums without
+// registers or barriers.  A row that does not start on a 16-byte boundary is covered by aligned vectors
+// all the same: its first and last vector are partly outside the row and masked.  A group's rows are a
+// multiple of 8 apart, so they all start at the same place in a vector and a thread holds the same
+// columns of each: gamma and beta are read once, and their gradients are summed in registers over the rows, then over
+// the CTA in shared memory, and one partial row per CTA goes to the workspace; a second kernel adds the
+// partial rows in a fixed order.  No atomics: the same bits on every run.
 #include <cuda_bf16.h>
+
+#include <algorithm>
 
 #include "svg2_device.cuh"
 #include "svg2_internal.h"
@@ -20,65 +27,48 @@ namespace {
 template <class T>
 struct NormArgs {
   const T *X, *dY;
-  const float *gamma, *beta;      // optional
-  const float *mean_in, *rstd_in; // backward
-  float *mean, *rstd;             // forward, optional
-  T* Y;                           // Y | dX
-  float* partial;                 // backward: [gridDim.x][2][W]
+  const float *gamma, *beta;       // optional
+  const float *mean_in, *rstd_in;  // backward
+  float *mean, *rstd;              // forward, optional
+  T* Y;                            // Y | dX
+  float* partial;                  // backward: [gridDim.x][2][W]
   long long rows;
   int W;
+  int x_mis;               // X's elements past a 16-byte boundary
+  bool dy_same, y_same;    // dY, Y start at the same place in a vector as X: 16-byte accesses fit
   float eps;
 };
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T>
+constexpr int kVec = 16 / static_cast<int>(sizeof(T));
 
-template <class T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = to_f32(*p);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 w = __ldg(reinterpret_cast<const float4*>(p));
-    v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-  } else {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// A vector as float pairs (the arithmetic runs on pairs: one instruction for two values).
+__device__ __forceinline__ void unpack(uint4 w, float2 (&v)[4]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[2 * e] = bf16lo_to_f32(u[e]), v[2 * e + 1] = bf16hi_to_f32(u[e]);
-  }
+  for (int e = 0; e < 4; ++e) v[e] = make_float2(bf16lo_to_f32(u[e]), bf16hi_to_f32(u[e]));
 }
-
-template <class T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    if constexpr (sizeof(T) == 4) *p = v[0];
-    else *p = __float2bfloat16(v[0]);
-  } else if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  }
+__device__ __forceinline__ void unpack(uint4 w, float2 (&v)[2]) {
+  v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+  v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
 }
-
-// float32 parameters of a thread's VEC columns
-template <int VEC>
-__device__ __forceinline__ void load_param(const float* p, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = __ldg(p);
-  } else {
-#pragma unroll
-    for (int e = 0; e < VEC; e += 4) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(p + e));
-      v[e] = w.x, v[e + 1] = w.y, v[e + 2] = w.z, v[e + 3] = w.w;
-    }
-  }
+__device__ __forceinline__ uint4 pack(const float2 (&v)[4]) {
+  return make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                    pack_bf16x2(v[3].x, v[3].y));
 }
+__device__ __forceinline__ uint4 pack(const float2 (&v)[2]) {
+  return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+}
+template <int P>
+__device__ __forceinline__ float element(const float2 (&v)[P], int e) { return (e & 1) ? v[e >> 1].y : v[e >> 1].x; }
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16(v); }
 
-// Sum of one value (or two) over a group of G threads: G lanes of a warp, or (G = 0) the whole CTA.
+// Sums of K values over a group of G threads: G lanes of a warp, or (G = 0) the whole CTA.
 // `turn` alternates the shared buffer between consecutive sums, so one barrier per sum is enough.
 template <int G, int K>
 __device__ __forceinline__ void group_sum(float (&v)[K], float* buf, int& turn) {
+  static_assert(K <= 8, "the shared buffer holds two sums of 8 values from 32 warps");
   constexpr int kWidth = G == 0 ? 32 : G;
 #pragma unroll
   for (int o = kWidth / 2; o > 0; o >>= 1)
@@ -86,7 +76,7 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float* buf, int& turn) 
     for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   if constexpr (G == 0) {
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* b = buf + turn * 64;
+    float* b = buf + turn * 256;
     turn ^= 1;
     if (lane == 0)
 #pragma unroll
@@ -102,193 +92,359 @@ __device__ __forceinline__ void group_sum(float (&v)[K], float* buf, int& turn) 
   }
 }
 
-// The columns of thread t of a group of n threads: vectors t, t + n, ... of the row.
-template <class T, int VEC, int G, int NV, int R, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const NormArgs<T> a) {
-  __shared__ float buf[128];
-  const int n = G == 0 ? blockDim.x : G;
-  const int t = threadIdx.x % n;
-  const int nvec = a.W / VEC;
-  const long long groups = static_cast<long long>(gridDim.x) * (blockDim.x / n);
-  const long long group = static_cast<long long>(blockIdx.x) * (blockDim.x / n) + threadIdx.x / n;
-  const float inv_w = 1.f / static_cast<float>(a.W);
-  int turn = 0;
-  // the trip count is the same for all groups of a CTA: the sums are collective
-  for (long long base = 0; base < a.rows; base += groups * R) {
-    float x[R][NV][VEC];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const long long row = base + r * groups + group;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = t + i * n;
-        if (row < a.rows && c < nvec) {
-          load_vec<T, VEC>(a.X + row * a.W + static_cast<long long>(c) * VEC, x[r][i]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) x[r][i][e] = 0.f;
-        }
-      }
+// Where a thread works: vectors t, t + n, ... of rows first, first + stride, ...; `off` elements of the first
+// vector lie before the row (the same for all its rows).
+template <class T, int G>
+struct Place {
+  int t, n, off, nvec;
+  long long first, stride;
+  __device__ __forceinline__ Place(const NormArgs<T>& a) {
+    constexpr int V = kVec<T>;
+    n = G == 0 ? blockDim.x : G;
+    t = threadIdx.x % n;
+    if constexpr (G == 0) {
+      first = blockIdx.x;
+      stride = gridDim.x;
+    } else {  // the groups of a warp are 8 rows apart, the 8 warps of a CTA take the rows between
+      constexpr int kPerWarp = 32 / G;
+      first = (static_cast<long long>(blockIdx.x) * kPerWarp + (threadIdx.x & 31) / G) * 8 + (threadIdx.x >> 5);
+      stride = static_cast<long long>(gridDim.x) * kPerWarp * 8;
     }
+    off = static_cast<int>((a.x_mis + first * a.W) % V);
+    nvec = (off + a.W + V - 1) / V;
+  }
+  // first column of vector i of this thread (may be negative or reach past W)
+  __device__ __forceinline__ int col(int i) const { return (t + i * n) * kVec<T> - off; }
+  __device__ __forceinline__ bool has(int i) const { return t + i * n < nvec; }
+};
+
+// Starts the copy of the vector at column c of a row into this thread's slot; zeros where `in` is false.  EDGE:
+// rows may start or end inside a vector.
+template <class T, bool EDGE>
+__device__ __forceinline__ void fetch_vec(uint4* slot, const T* X, bool same, bool in, long long row, int c,
+                                          const NormArgs<T>& a) {
+  constexpr int V = kVec<T>;
+  const long long e0 = row * a.W + c;
+  if constexpr (!EDGE) {
+    cp_async16_zfill(smem_u32(slot), X + (in ? e0 : 0), in);
+  } else if (!in || (same && e0 >= 0 && e0 + V <= a.rows * a.W)) {
+    cp_async16_zfill(smem_u32(slot), X + (in ? e0 : 0), in);
+  } else {  // the tensor's ends, or another alignment than X's: only the row's own elements
+    T* s = reinterpret_cast<T*>(slot);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const long long row = base + r * groups + group;
-      float s[1] = {0.f};
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s[0] += x[r][i][e];
-      group_sum<G, 1>(s, buf, turn);
-      const float mean = s[0] * inv_w;
-      s[0] = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const bool in = t + i * n < nvec;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          x[r][i][e] = in ? x[r][i][e] - mean : 0.f;
-          s[0] = fmaf(x[r][i][e], x[r][i][e], s[0]);
-        }
-      }
-      group_sum<G, 1>(s, buf, turn);
-      const float rstd = 1.f / sqrtf(fmaf(s[0], inv_w, a.eps));
-      if (row >= a.rows) continue;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = t + i * n;
-        if (c >= nvec) continue;
-        float y[VEC], p[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) y[e] = x[r][i][e] * rstd;
-        if (a.gamma != nullptr) {
-          load_param<VEC>(a.gamma + c * VEC, p);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) y[e] *= p[e];
-        }
-        if (a.beta != nullptr) {
-          load_param<VEC>(a.beta + c * VEC, p);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) y[e] += p[e];
-        }
-        store_vec<T, VEC>(a.Y + row * a.W + static_cast<long long>(c) * VEC, y);
-      }
-      if (t == 0) {
-        if (a.mean != nullptr) a.mean[row] = mean;
-        if (a.rstd != nullptr) a.rstd[row] = rstd;
-      }
-    }
+    for (int e = 0; e < V; ++e)
+      if (c + e >= 0 && c + e < a.W) s[e] = X[e0 + e];
   }
 }
 
-template <class T, int VEC, int G, int NV, int R, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs<T> a) {
-  __shared__ float buf[128];
-  __shared__ float acc_s[G == 0 ? 1 : 2 * 8 * 32 * NV * VEC];  // the warps' column sums
-  const int n = G == 0 ? blockDim.x : G;
-  const int t = threadIdx.x % n;
-  const int nvec = a.W / VEC;
-  const long long groups = static_cast<long long>(gridDim.x) * (blockDim.x / n);
-  const long long group = static_cast<long long>(blockIdx.x) * (blockDim.x / n) + threadIdx.x / n;
-  const float inv_w = 1.f / static_cast<float>(a.W);
-  int turn = 0;
-  float dg[NV][VEC], db[NV][VEC];
+// The part of a vector that lies inside its row, the same for all rows of a thread: elements [lo, hi).
+struct Span {
+  int lo, hi;
+};
+
+// Bits of the elements inside the span, to clear what a neighbouring row left in the vector.
+template <class T>
+__device__ __forceinline__ uint4 span_bits(Span p) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) dg[i][e] = db[i][e] = 0.f;
-  for (long long base = 0; base < a.rows; base += groups * R) {
-    float x[R][NV][VEC], g[R][NV][VEC], rstd[R], mean[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const long long row = base + r * groups + group;
-      const bool live = row < a.rows;
-      mean[r] = live ? __ldg(a.mean_in + row) : 0.f;
-      rstd[r] = live ? __ldg(a.rstd_in + row) : 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = t + i * n;
-        if (live && c < nvec) {
-          load_vec<T, VEC>(a.X + row * a.W + static_cast<long long>(c) * VEC, x[r][i]);
-          load_vec<T, VEC>(a.dY + row * a.W + static_cast<long long>(c) * VEC, g[r][i]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) x[r][i][e] = mean[r], g[r][i][e] = 0.f;
-        }
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const long long row = base + r * groups + group;
-      float s[2] = {0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = t + i * n;
-        float p[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) p[e] = 1.f;
-        if (a.gamma != nullptr && c < nvec) load_param<VEC>(a.gamma + c * VEC, p);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          x[r][i][e] = (x[r][i][e] - mean[r]) * rstd[r];
-          dg[i][e] = fmaf(g[r][i][e], x[r][i][e], dg[i][e]);
-          db[i][e] += g[r][i][e];
-          g[r][i][e] *= p[e];
-          s[0] += g[r][i][e];
-          s[1] = fmaf(g[r][i][e], x[r][i][e], s[1]);
-        }
-      }
-      group_sum<G, 2>(s, buf, turn);
-      if (row >= a.rows) continue;
-      const float c1 = s[0] * inv_w, c2 = s[1] * inv_w;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = t + i * n;
-        if (c >= nvec) continue;
-        float d[VEC];
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) d[e] = rstd[r] * (g[r][i][e] - c1 - x[r][i][e] * c2);
-        store_vec<T, VEC>(a.Y + row * a.W + static_cast<long long>(c) * VEC, d);
-      }
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      w[k] = (k >= p.lo && k < p.hi) ? 0xffffffffu : 0u;
+    } else {
+      w[k] = ((2 * k >= p.lo && 2 * k < p.hi) ? 0xffffu : 0u) | ((2 * k + 1 >= p.lo && 2 * k + 1 < p.hi) ? 0xffff0000u : 0u);
     }
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 operator&(uint4 a, uint4 b) { return make_uint4(a.x & b.x, a.y & b.y, a.z & b.z, a.w & b.w); }
+
+template <class T, bool EDGE>
+__device__ __forceinline__ void put_vec(T* Y, bool same, long long row, int c, Span in, const float2 (&v)[kVec<T> / 2],
+                                        int W) {
+  constexpr int V = kVec<T>;
+  T* p = Y + row * W + c;
+  if (!EDGE || (same && in.lo == 0 && in.hi == V)) {
+    *reinterpret_cast<uint4*>(p) = pack(v);
+  } else if (sizeof(T) == 2 && same && (in.lo == 0 || in.hi == V)) {
+    // the row's first or last vector: its 1 to 7 elements as at most one store each of 2, 4 and 8 bytes
+    const uint4 w = pack(v);
+    char* q = reinterpret_cast<char*>(p);
+    if (in.hi == V) {
+      const int h = V - in.lo;
+      if (h & 1) *reinterpret_cast<uint16_t*>(q + 2 * in.lo) = static_cast<uint16_t>((h > 4 ? (h > 6 ? w.x : w.y) : (h > 2 ? w.z : w.w)) >> 16);
+      if (h & 2) *reinterpret_cast<uint32_t*>(q + (h & 4 ? 4 : 12)) = h & 4 ? w.y : w.w;
+      if (h & 4) *reinterpret_cast<uint2*>(q + 8) = make_uint2(w.z, w.w);
+    } else {
+      const int h = in.hi;
+      if (h & 4) *reinterpret_cast<uint2*>(q) = make_uint2(w.x, w.y);
+      if (h & 2) *reinterpret_cast<uint32_t*>(q + (h & 4 ? 8 : 0)) = h & 4 ? w.z : w.x;
+      if (h & 1) *reinterpret_cast<uint16_t*>(q + 2 * (h - 1)) = static_cast<uint16_t>(h > 4 ? (h > 6 ? w.w : w.z) : (h > 2 ? w.y : w.x));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e >= in.lo && e < in.hi) store_one(p + e, element(v, e));
+  }
+}
+
+// float32 parameters of a thread's columns (`none` where there are none)
+template <int P>
+__device__ __forceinline__ void load_param(const float* p, int c, int W, float none, float2 (&v)[P]) {
+  auto one = [&](int i) { return (p != nullptr && i >= 0 && i < W) ? __ldg(p + i) : none; };
+#pragma unroll
+  for (int e = 0; e < P; ++e) v[e] = make_float2(one(c + 2 * e), one(c + 2 * e + 1));
+}
+
+template <class T, bool EDGE, int G, int NV, int R, int STAGES, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const NormArgs<T> a) {
+  constexpr int V = kVec<T>, P = V / 2;
+  extern __shared__ uint4 ring[];  // [STAGES][R][NV][blockDim.x]
+  __shared__ float buf[512];
+  const Place<T, G> at(a);
+  const float inv_w = 1.f / static_cast<float>(a.W);
+  int turn = 0;
+  auto slot = [&](int stage, int r, int i) { return ring + ((stage * R + r) * NV + i) * blockDim.x + threadIdx.x; };
+  auto fetch = [&](long long base, int stage) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = base + r * at.stride + at.first;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        fetch_vec<T, EDGE>(slot(stage, r, i), a.X, true, row < a.rows && at.has(i), row, at.col(i), a);
+    }
+    cp_async_commit();
+  };
+  const long long step = at.stride * R;
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(s * step, s);
+  float2 ga[NV][P], be[NV][P];  // of this thread's columns
+  float2 keep[NV][P];            // 1 inside the row, 0 outside (EDGE)
+  Span span[NV];
+  uint4 bits[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    span[i] = Span{max(0, -at.col(i)), min(V, a.W - at.col(i))};
+    bits[i] = span_bits<T>(span[i]);
+#pragma unroll
+    for (int e = 0; e < P; ++e)
+      keep[i][e] = make_float2(2 * e >= span[i].lo && 2 * e < span[i].hi ? 1.f : 0.f,
+                               2 * e + 1 >= span[i].lo && 2 * e + 1 < span[i].hi ? 1.f : 0.f);
+    load_param(a.gamma, at.col(i), a.W, 1.f, ga[i]);
+    load_param(a.beta, at.col(i), a.W, 0.f, be[i]);
+  }
+  int stage = 0;
+  // the trip count is the same for all groups of a CTA: the sums are collective
+  for (long long base = 0; base < a.rows; base += step) {
+    fetch(base + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+    cp_async_wait<STAGES - 1>();
+    float2 x[R][NV][P];
+    float s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        unpack(EDGE ? *slot(stage, r, i) & bits[i] : *slot(stage, r, i), x[r][i]);
+#pragma unroll
+        for (int e = 0; e < P; ++e) t = add2(t, x[r][i][e]);
+      }
+      s[r] = t.x + t.y;
+    }
+    group_sum<G, R>(s, buf, turn);
+    float mean[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = s[r] * inv_w;
+      const float2 neg = make_float2(-mean[r], -mean[r]);
+      float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) x[r][i][e] = add2(x[r][i][e], neg);
+        if (EDGE || at.has(i))
+#pragma unroll
+          for (int e = 0; e < P; ++e) t = fma2(x[r][i][e], EDGE ? mul2(x[r][i][e], keep[i][e]) : x[r][i][e], t);
+      }
+      s[r] = t.x + t.y;
+    }
+    group_sum<G, R>(s, buf, turn);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = base + r * at.stride + at.first;
+      const float rstd = rsqrtf(fmaf(s[r], inv_w, a.eps));
+      const float2 r2 = make_float2(rstd, rstd);
+      if (row < a.rows) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          if (!at.has(i)) continue;
+          float2 y[P];
+#pragma unroll
+          for (int e = 0; e < P; ++e) y[e] = fma2(mul2(x[r][i][e], r2), ga[i][e], be[i][e]);
+          put_vec<T, EDGE>(a.Y, a.y_same, row, at.col(i), span[i], y, a.W);
+        }
+        if (at.t == 0) {
+          if (a.mean != nullptr) a.mean[row] = mean[r];
+          if (a.rstd != nullptr) a.rstd[row] = rstd;
+        }
+      }
+    }
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
+}
+
+template <class T, bool EDGE, int G, int NV, int R, int STAGES, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs<T> a) {
+  constexpr int V = kVec<T>, P = V / 2;
+  // [STAGES][R][2][NV][blockDim.x], then gamma of each thread's columns [NV][V / 4][blockDim.x]; at the end the
+  // warps' column sums [8][2][W]
+  extern __shared__ uint4 ring[];
+  __shared__ float buf[512];
+  const Place<T, G> at(a);
+  const float inv_w = 1.f / static_cast<float>(a.W);
+  int turn = 0;
+  auto slot = [&](int stage, int r, int k, int i) {
+    return ring + (((stage * R + r) * 2 + k) * NV + i) * blockDim.x + threadIdx.x;
+  };
+  auto gamma_slot = [&](int i, int q) {
+    return reinterpret_cast<float4*>(ring + STAGES * R * 2 * NV * blockDim.x + (i * (V / 4) + q) * blockDim.x + threadIdx.x);
+  };
+  auto fetch = [&](long long base, int stage) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = base + r * at.stride + at.first;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const bool in = row < a.rows && at.has(i);
+        fetch_vec<T, EDGE>(slot(stage, r, 0, i), a.X, true, in, row, at.col(i), a);
+        fetch_vec<T, EDGE>(slot(stage, r, 1, i), a.dY, a.dy_same, in, row, at.col(i), a);
+      }
+    }
+    cp_async_commit();
+  };
+  const long long step = at.stride * R;
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(s * step, s);
+  float2 dg[NV][P], db[NV][P];
+  Span span[NV];
+  uint4 bits[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    span[i] = Span{max(0, -at.col(i)), min(V, a.W - at.col(i))};
+    bits[i] = span_bits<T>(span[i]);
+    float2 p[P];
+    load_param(a.gamma, at.col(i), a.W, 1.f, p);
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q) *gamma_slot(i, q) = make_float4(p[2 * q].x, p[2 * q].y, p[2 * q + 1].x, p[2 * q + 1].y);
+#pragma unroll
+    for (int e = 0; e < P; ++e) dg[i][e] = db[i][e] = make_float2(0.f, 0.f);
+  }
+  int stage = 0;
+  float mean[R], rstd[R];  // of the next rows, read ahead
+  auto stats = [&](long long base) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = base + r * at.stride + at.first;
+      mean[r] = row < a.rows ? __ldg(a.mean_in + row) : 0.f;
+      rstd[r] = row < a.rows ? __ldg(a.rstd_in + row) : 0.f;
+    }
+  };
+  stats(0);
+  for (long long base = 0; base < a.rows; base += step) {
+    fetch(base + (STAGES - 1) * step, stage == 0 ? STAGES - 1 : stage - 1);
+    float m[R], rs[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) m[r] = mean[r], rs[r] = rstd[r];
+    stats(base + step);
+    cp_async_wait<STAGES - 1>();
+    float2 x[R][NV][P], g[R][NV][P];
+    float s[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float2 neg = make_float2(-m[r], -m[r]), r2 = make_float2(rs[r], rs[r]);
+      float2 t0 = make_float2(0.f, 0.f), t1 = t0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        unpack(EDGE ? *slot(stage, r, 0, i) & bits[i] : *slot(stage, r, 0, i), x[r][i]);
+        // (dY is 0 outside the row: nothing is added there)
+        unpack(EDGE ? *slot(stage, r, 1, i) & bits[i] : *slot(stage, r, 1, i), g[r][i]);
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) {
+          const float4 p4 = *gamma_slot(i, q);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int e = 2 * q + u;
+            x[r][i][e] = mul2(add2(x[r][i][e], neg), r2);
+            dg[i][e] = fma2(g[r][i][e], x[r][i][e], dg[i][e]);
+            db[i][e] = add2(db[i][e], g[r][i][e]);
+            g[r][i][e] = mul2(g[r][i][e], u == 0 ? make_float2(p4.x, p4.y) : make_float2(p4.z, p4.w));
+            t0 = add2(t0, g[r][i][e]);
+            t1 = fma2(g[r][i][e], x[r][i][e], t1);
+          }
+        }
+      }
+      s[2 * r] = t0.x + t0.y;
+      s[2 * r + 1] = t1.x + t1.y;
+    }
+    group_sum<G, 2 * R>(s, buf, turn);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const long long row = base + r * at.stride + at.first;
+      if (row >= a.rows) continue;
+      const float c1 = -s[2 * r] * inv_w, c2 = -s[2 * r + 1] * inv_w;
+      const float2 c12 = make_float2(c1, c1), c22 = make_float2(c2, c2), r2 = make_float2(rs[r], rs[r]);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!at.has(i)) continue;
+        float2 d[P];
+#pragma unroll
+        for (int e = 0; e < P; ++e) d[e] = mul2(r2, fma2(x[r][i][e], c22, add2(g[r][i][e], c12)));
+        put_vec<T, EDGE>(a.Y, a.y_same, row, at.col(i), span[i], d, a.W);
+      }
+    }
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
   float* out = a.partial + static_cast<size_t>(blockIdx.x) * 2 * a.W;
   if constexpr (G == 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * n;
-      if (c >= nvec) continue;
+      const int c = at.col(i);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        out[c * VEC + e] = dg[i][e];
-        out[a.W + c * VEC + e] = db[i][e];
-      }
+      for (int e = 0; e < V; ++e)
+        if (c + e >= 0 && c + e < a.W) {
+          out[c + e] = element(dg[i], e);
+          out[a.W + c + e] = element(db[i], e);
+        }
     }
   } else {
-    // over the groups of a warp by shuffles, over the 8 warps in shared memory
+    // over the groups of a warp by shuffles (they hold the same columns), over the 8 warps in shared memory
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* cols = reinterpret_cast<float*>(ring);
+    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      const int c = at.col(i);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
+      for (int e = 0; e < V; ++e) {
+        float u = element(dg[i], e), v = element(db[i], e);
 #pragma unroll
         for (int o = G; o < 32; o <<= 1) {
-          dg[i][e] += __shfl_xor_sync(0xffffffffu, dg[i][e], o);
-          db[i][e] += __shfl_xor_sync(0xffffffffu, db[i][e], o);
+          u += __shfl_xor_sync(0xffffffffu, u, o);
+          v += __shfl_xor_sync(0xffffffffu, v, o);
         }
-        if (lane < G) {
-          acc_s[((warp * 2 + 0) * NV + i) * VEC * G + lane * VEC + e] = dg[i][e];
-          acc_s[((warp * 2 + 1) * NV + i) * VEC * G + lane * VEC + e] = db[i][e];
+        if (lane < G && c + e >= 0 && c + e < a.W) {
+          cols[(warp * 2 + 0) * a.W + c + e] = u;
+          cols[(warp * 2 + 1) * a.W + c + e] = v;
         }
       }
+    }
     __syncthreads();
-    constexpr int kCols = NV * VEC * G;  // column c of the row is entry c: vector c / VEC = lane + i G
-    for (int c = threadIdx.x; c < 2 * kCols; c += blockDim.x) {
-      const int which = c / kCols, col = c % kCols;
-      if (col >= a.W) continue;
+    for (int c = threadIdx.x; c < 2 * a.W; c += blockDim.x) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) s += acc_s[(w * 2 + which) * kCols + col];
-      out[which * a.W + col] = s;
+      for (int w = 0; w < 8; ++w) s += cols[w * 2 * a.W + c];
+      out[c] = s;
     }
   }
 }
@@ -318,45 +474,60 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
   }
 }
 
-template <class T, int VEC, int G, int NV, int R, int MAXT = 256>
-cudaError_t run_norm(const NormArgs<T>& a, bool bwd, int threads, int max_parts, int* parts, cudaStream_t s) {
+template <class T, bool BWD, bool EDGE, int G, int NV, int R, int STAGES, int MAXT>
+cudaError_t run_norm(const NormArgs<T>& a, int threads, int max_parts, int* parts, cudaStream_t s) {
+  constexpr int V = kVec<T>;
+  constexpr auto kernel =
+      BWD ? norm_bwd_kernel<T, EDGE, G, NV, R, STAGES, MAXT> : norm_fwd_kernel<T, EDGE, G, NV, R, STAGES, MAXT>;
   const int per_cta = G == 0 ? 1 : threads / G;
-  // as many CTAs as are resident at once (every group then meets the same number of rows, within one pass)
-  int resident = 0;
-  cudaError_t e = bwd ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, norm_bwd_kernel<T, VEC, G, NV, R, MAXT>, threads, 0)
-                      : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, norm_fwd_kernel<T, VEC, G, NV, R, MAXT>, threads, 0);
+  size_t smem = static_cast<size_t>(STAGES) * R * (BWD ? 2 : 1) * NV * threads * 16;
+  if (BWD) smem += static_cast<size_t>(NV) * V * threads * 4;
+  if (BWD && G != 0) smem = std::max(smem, static_cast<size_t>(16) * a.W * 4);
+  cudaError_t e = cudaSuccess;
+  // (48 KB, less the static buffer, need no permission)
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const long long want = (a.rows + static_cast<long long>(per_cta) * R - 1) / (static_cast<long long>(per_cta) * R);
-  long long grid = static_cast<long long>(kNormSms) * (resident > 0 ? resident : 1);
-  if (grid > want) grid = want;
-  if (bwd && grid > max_parts) grid = max_parts;
+  long long grid = (a.rows + per_cta - 1) / per_cta;
+  if (grid > kNormSms) {  // as many CTAs as are resident at once
+    int resident = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, smem);
+    if (e != cudaSuccess) return e;
+    const long long most = static_cast<long long>(kNormSms) * std::max(1, std::min(resident, kNormMaxPerSm));
+    if (grid > most) grid = most;
+  }
+  if (BWD && grid > max_parts) grid = max_parts;
+  if (EDGE && G == 0 && grid < a.rows) grid = std::max(8LL, grid / 8 * 8);  // a CTA's rows are a multiple of 8 apart
   *parts = static_cast<int>(grid);
-  if (bwd) norm_bwd_kernel<T, VEC, G, NV, R, MAXT><<<static_cast<unsigned>(grid), threads, 0, s>>>(a);
-  else norm_fwd_kernel<T, VEC, G, NV, R, MAXT><<<static_cast<unsigned>(grid), threads, 0, s>>>(a);
+  kernel<<<static_cast<unsigned>(grid), threads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <class T, int VEC>
-cudaError_t pick_norm(const NormArgs<T>& a, bool bwd, int max_parts, int* parts, cudaStream_t s) {
-  const int nvec = a.W / VEC;
-  // a row of up to 128 vectors belongs to lanes of one warp, a longer one to a CTA
-  if constexpr (VEC > 1) {
-    if (nvec <= 8) return run_norm<T, VEC, 8, 1, 2>(a, bwd, 256, max_parts, parts, s);
-    if (nvec <= 16) return run_norm<T, VEC, 16, 1, 2>(a, bwd, 256, max_parts, parts, s);
-    if (nvec <= 32) return run_norm<T, VEC, 32, 1, 2>(a, bwd, 256, max_parts, parts, s);
-    if (nvec <= 64) return run_norm<T, VEC, 32, 2, 1>(a, bwd, 256, max_parts, parts, s);
-    if (nvec <= 256) return run_norm<T, VEC, 0, 1, 1>(a, bwd, (nvec + 31) / 32 * 32, max_parts, parts, s);
-    // (at most 8192 columns: 1024 vectors of bf16, 2048 of float32)
-    return run_norm<T, VEC, 0, 2, 1, VEC == 8 ? 512 : 1024>(a, bwd, ((nvec + 1) / 2 + 31) / 32 * 32, max_parts, parts, s);
-  } else {
-    if (nvec <= 32) return run_norm<T, 1, 32, 1, 2>(a, bwd, 256, max_parts, parts, s);
-    if (nvec <= 128) return run_norm<T, 1, 32, 4, 1>(a, bwd, 256, max_parts, parts, s);
-    if (nvec <= 1024) return run_norm<T, 1, 0, 4, 1>(a, bwd, ((nvec + 3) / 4 + 31) / 32 * 32, max_parts, parts, s);
-    return run_norm<T, 1, 0, 8, 1, 1024>(a, bwd, ((nvec + 7) / 8 + 31) / 32 * 32, max_parts, parts, s);
+template <class T, bool BWD, bool EDGE>
+cudaError_t pick_norm(const NormArgs<T>& a, int max_parts, int* parts, cudaStream_t s) {
+  constexpr int V = kVec<T>;
+  // vectors that cover a row, wherever it starts
+  const int nvec = EDGE ? (V - 1 + a.W + V - 1) / V : a.W / V;
+  auto cta = [&](int nv) { return ((nvec + nv - 1) / nv + 31) / 32 * 32; };
+  // Rows at a time (R) and ring stages (S) are the fastest of a sweep over R in 1, 2, 4, S in 2, 3, 4 and, for a CTA
+  // per row, 1 to 5 vectors a thread: more rows share a barrier, more registers leave fewer CTAs resident.
+  // bf16, 3024000 x 128: forward 254 us (R = 2, S = 2) against 299 to 309 for the others, backward 367 us (R = 1, S = 4)
+  // against 391 to 423; 75600 x 5120: forward 241 us (5 vectors, R = 2) against 247 to 371, backward 418 us
+  // (5 vectors, R = 1) against 424 to 553; 200000 x 1024: 135 and 218 us (2 vectors, R = 4) against 141 to 165 and
+  // 219 to 272.  Copying the same bytes takes 237, 355, 237, 355, 125 and 188 us.
+  constexpr int R1 = BWD ? 1 : 2, S1 = BWD ? 4 : 2;
+  if (nvec <= 8) return run_norm<T, BWD, EDGE, 8, 1, R1, S1, 256>(a, 256, max_parts, parts, s);
+  if (nvec <= 16) return run_norm<T, BWD, EDGE, 16, 1, R1, S1, 256>(a, 256, max_parts, parts, s);
+  if (nvec <= 32) return run_norm<T, BWD, EDGE, 32, 1, R1, S1, 256>(a, 256, max_parts, parts, s);
+  if (nvec <= 64) return run_norm<T, BWD, EDGE, 32, 2, 1, BWD ? 3 : 2, 256>(a, 256, max_parts, parts, s);
+  if (nvec <= 256) {
+    if constexpr (BWD && EDGE) return run_norm<T, BWD, EDGE, 0, 2, 1, 4, 128>(a, cta(2), max_parts, parts, s);
+    else if constexpr (V == 8) return run_norm<T, BWD, EDGE, 0, 2, 4, 2, 128>(a, cta(2), max_parts, parts, s);
+    else return run_norm<T, BWD, EDGE, 0, 1, 4, 2, 256>(a, cta(1), max_parts, parts, s);
   }
+  if (nvec <= 1024) return run_norm<T, BWD, EDGE, 0, 5, BWD ? 1 : 2, BWD ? 3 : 2, 224>(a, cta(5), max_parts, parts, s);
+  // (at most 8192 columns: 1025 vectors of bf16, 2049 of float32)
+  return run_norm<T, BWD, EDGE, 0, 4, 1, 2, V == 8 ? 288 : 544>(a, cta(4), max_parts, parts, s);
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <class T>
 cudaError_t run_typed(const NormCall& n, bool bwd, cudaStream_t s) {
@@ -372,13 +543,17 @@ cudaError_t run_typed(const NormCall& n, bool bwd, cudaStream_t s) {
   a.rows = n.rows;
   a.W = n.width;
   a.eps = n.eps;
-  constexpr int kVec = 16 / sizeof(T);
-  // 16-byte accesses where every row starts on a 16-byte boundary, else element by element
-  const bool vec = n.width % kVec == 0 && aligned16(n.X) && aligned16(n.dY) && aligned16(n.Y) && aligned16(n.gamma) &&
-                   aligned16(n.beta);
+  auto mis = [](const void* p) { return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T)); };
+  a.x_mis = mis(n.X);
+  a.dy_same = mis(n.dY) == a.x_mis;
+  a.y_same = mis(n.Y) == a.x_mis;
   int parts = 0;
   const int max_parts = norm_max_parts(n.rows);
-  cudaError_t e = vec ? pick_norm<T, kVec>(a, bwd, max_parts, &parts, s) : pick_norm<T, 1>(a, bwd, max_parts, &parts, s);
+  const bool edge = a.W % kVec<T> != 0 || a.x_mis != 0 || !a.y_same || (bwd && !a.dy_same);
+  cudaError_t e = bwd ? (edge ? pick_norm<T, true, true>(a, max_parts, &parts, s)
+                              : pick_norm<T, true, false>(a, max_parts, &parts, s))
+                      : (edge ? pick_norm<T, false, true>(a, max_parts, &parts, s)
+                              : pick_norm<T, false, false>(a, max_parts, &parts, s));
   if (e == cudaSuccess && bwd && (n.dgamma != nullptr || n.dbeta != nullptr)) {
     norm_reduce_kernel<<<(2 * n.width + 31) / 32, 1024, 0, s>>>(n.partial, parts, n.width, n.dgamma, n.dbeta);
     e = cudaGetLastError();

@@ -398,25 +398,52 @@ def svg2_sparse_attn_noalloc(Qp: torch.Tensor, Kp: torch.Tensor, Vp: torch.Tenso
                                           _p(device_status), _stream(stream)), "svg2_sparse_attn_noalloc")
 
 
-def _one_device(*tensors):
-    """The training calls launch on the current device's stream: every tensor must live there."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) > 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
-    dev = next(iter(devices))
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+def _device() -> int:
+    return torch.cuda.current_device()
+
+
+def _ptr(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int, dev: int) -> int:
+    """_arg for the training calls, in one pass (their smallest calls are bound by the host): dtype, room for
+    `numel` elements, contiguity, and the current device `dev`, whose stream the call launches on."""
+    if t is not None and t.dtype is dtype and t.numel() >= numel and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, the call runs on the current device cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: libsvg2 takes contiguous tensors")
+    _arg(t, name, (dtype,), numel)
+    raise ValueError(f"{name}: refused")
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, numel: int, dev: int) -> Optional[int]:
+    return None if t is None else _ptr(t, name, dtype, numel, dev)
+
+
+def _plan_ptrs(Q, K, V, q_off, k_off, sel_count, sel_idx, dev):
+    """Sizes and checked pointers of a sparse training call's operands and plan."""
+    B, H, N, d = _dims(Q, "Qp")
+    if q_off is None or k_off is None or q_off.dim() < 1 or k_off.dim() < 1:
+        raise ValueError("q_off and k_off are required")
+    BH, n, i32, bf16 = B * H, B * H * N * d, torch.int32, torch.bfloat16
+    nQ, nK = int(q_off.shape[-1]) - 1, int(k_off.shape[-1]) - 1
+    return B, H, N, d, nQ, nK, (
+        _ptr(Q, "Qp", bf16, 0, dev), _ptr(K, "Kp", bf16, n, dev), _ptr(V, "Vp", bf16, n, dev),
+        _ptr(q_off, "q_off", i32, BH * (nQ + 1), dev), _ptr(k_off, "k_off", i32, BH * (nK + 1), dev),
+        _ptr(sel_count, "sel_count", i32, BH * nQ, dev), _ptr(sel_idx, "sel_idx", i32, BH * nQ * nK, dev))
 
 
 def svg2_dense_attn_lse(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float, O: torch.Tensor,
                         lse: torch.Tensor, ws: torch.Tensor, stream=None):
     """svg2_dense_attn that also writes the rows' log-sum-exp (for svg2_dense_attn_bwd)."""
     B, H, N, d = _dims(Q, "Q")
-    n = B * H * N * d
-    _one_device(Q, K, V, O, lse, ws)
-    _check(lib().svg2_dense_attn_lse(_arg(Q, "Q", _BF16, 0), _arg(K, "K", _BF16, n), _arg(V, "V", _BF16, n), B, H, N, d,
-                                     float(scale), _arg(O, "O", _BF16, n), _arg(lse, "lse", _F32, B * H * N), _p(ws),
-                                     _nbytes(ws), _stream(stream)), "svg2_dense_attn_lse")
+    n, dev, bf16 = B * H * N * d, _device(), torch.bfloat16
+    _check(lib().svg2_dense_attn_lse(_ptr(Q, "Q", bf16, 0, dev), _ptr(K, "K", bf16, n, dev), _ptr(V, "V", bf16, n, dev),
+                                     B, H, N, d, float(scale), _ptr(O, "O", bf16, n, dev),
+                                     _ptr(lse, "lse", torch.float32, B * H * N, dev),
+                                     _ptr(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream(stream)),
+           "svg2_dense_attn_lse")
 
 
 def svg2_sparse_attn_lse(Qp: torch.Tensor, Kp: torch.Tensor, Vp: torch.Tensor, q_off: torch.Tensor,
@@ -424,10 +451,14 @@ def svg2_sparse_attn_lse(Qp: torch.Tensor, Kp: torch.Tensor, Vp: torch.Tensor, q
                          O: torch.Tensor, lse: torch.Tensor, ws: torch.Tensor, perm_q: Optional[torch.Tensor] = None,
                          stream=None):
     """svg2_sparse_attn that also writes the log-sum-exp by permuted row (for svg2_sparse_attn_bwd)."""
-    B, H, N, d, nQ, nK, ptr = _attn_args(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, O, perm_q)
-    _one_device(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, O, lse, ws, perm_q)
-    _check(lib().svg2_sparse_attn_lse(*ptr[:7], B, H, N, d, nQ, nK, float(scale), ptr[8], ptr[7],
-                                      _arg(lse, "lse", _F32, B * H * N), _p(ws), _nbytes(ws), _stream(stream)),
+    dev = _device()
+    B, H, N, d, nQ, nK, ptr = _plan_ptrs(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, dev)
+    rows = B * H * N
+    _check(lib().svg2_sparse_attn_lse(*ptr, B, H, N, d, nQ, nK, float(scale),
+                                      _opt(perm_q, "perm_q", torch.int32, rows, dev),
+                                      _ptr(O, "O", torch.bfloat16, rows * d, dev),
+                                      _ptr(lse, "lse", torch.float32, rows, dev),
+                                      _ptr(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream(stream)),
            "svg2_sparse_attn_lse")
 
 
@@ -448,12 +479,12 @@ def svg2_dense_attn_bwd(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, O: to
                         ws: torch.Tensor, stream=None):
     """Gradients of dense attention from O and lse as svg2_dense_attn_lse wrote them."""
     B, H, N, d = _dims(Q, "Q")
-    n = B * H * N * d
-    _one_device(Q, K, V, O, lse, dO, dQ, dK, dV, ws)
-    _check(lib().svg2_dense_attn_bwd(_arg(Q, "Q", _BF16, 0), _arg(K, "K", _BF16, n), _arg(V, "V", _BF16, n),
-                                     _arg(O, "O", _BF16, n), _arg(lse, "lse", _F32, B * H * N),
-                                     _arg(dO, "dO", _BF16, n), B, H, N, d, float(scale), _arg(dQ, "dQ", _BF16, n),
-                                     _arg(dK, "dK", _BF16, n), _arg(dV, "dV", _BF16, n), _p(ws), _nbytes(ws),
+    n, dev, bf16 = B * H * N * d, _device(), torch.bfloat16
+    _check(lib().svg2_dense_attn_bwd(_ptr(Q, "Q", bf16, 0, dev), _ptr(K, "K", bf16, n, dev), _ptr(V, "V", bf16, n, dev),
+                                     _ptr(O, "O", bf16, n, dev), _ptr(lse, "lse", torch.float32, B * H * N, dev),
+                                     _ptr(dO, "dO", bf16, n, dev), B, H, N, d, float(scale),
+                                     _ptr(dQ, "dQ", bf16, n, dev), _ptr(dK, "dK", bf16, n, dev),
+                                     _ptr(dV, "dV", bf16, n, dev), _ptr(ws, "ws", torch.uint8, 0, dev), ws.numel(),
                                      _stream(stream)), "svg2_dense_attn_bwd")
 
 
@@ -477,14 +508,17 @@ def svg2_sparse_attn_bwd(Qp: torch.Tensor, Kp: torch.Tensor, Vp: torch.Tensor, O
                          perm_k: Optional[torch.Tensor] = None, stream=None):
     """Gradients of the sparse attention for its plan: O, dO and dQ by token when perm_q is given, dK and dV by
     token when perm_k is."""
-    B, H, N, d, nQ, nK, ptr = _attn_args(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, O, perm_q)
-    _one_device(Qp, Kp, Vp, O, lse, dO, q_off, k_off, sel_count, sel_idx, dQ, dK, dV, ws, perm_q, perm_k)
-    BH, n = B * H, B * H * N * d
-    _check(lib().svg2_sparse_attn_bwd(*ptr[:3], ptr[7], _arg(lse, "lse", _F32, BH * N), _arg(dO, "dO", _BF16, n),
-                                      *ptr[3:7], B, H, N, d, nQ, nK, float(scale), ptr[8],
-                                      _arg(perm_k, "perm_k", _I32, BH * N, optional=True), _arg(dQ, "dQ", _BF16, n),
-                                      _arg(dK, "dK", _BF16, n), _arg(dV, "dV", _BF16, n), _p(ws), _nbytes(ws),
-                                      _stream(stream)), "svg2_sparse_attn_bwd")
+    dev, bf16 = _device(), torch.bfloat16
+    B, H, N, d, nQ, nK, ptr = _plan_ptrs(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, dev)
+    rows = B * H * N
+    n = rows * d
+    _check(lib().svg2_sparse_attn_bwd(*ptr[:3], _ptr(O, "O", bf16, n, dev), _ptr(lse, "lse", torch.float32, rows, dev),
+                                      _ptr(dO, "dO", bf16, n, dev), *ptr[3:], B, H, N, d, nQ, nK, float(scale),
+                                      _opt(perm_q, "perm_q", torch.int32, rows, dev),
+                                      _opt(perm_k, "perm_k", torch.int32, rows, dev), _ptr(dQ, "dQ", bf16, n, dev),
+                                      _ptr(dK, "dK", bf16, n, dev), _ptr(dV, "dV", bf16, n, dev),
+                                      _ptr(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream(stream)),
+           "svg2_sparse_attn_bwd")
 
 
 def _rows(X: torch.Tensor, name: str):
@@ -499,11 +533,11 @@ def svg2_layer_norm(X: torch.Tensor, gamma: Optional[torch.Tensor], beta: Option
                     stream=None):
     """Layer norm of X [..., width] over its last dimension; mean and rstd [rows] are kept for the gradients."""
     rows, width = _rows(X, "X")
-    _one_device(X, gamma, beta, Y, mean, rstd)
-    _check(lib().svg2_layer_norm(_arg(X, "X", _DATA, 0), _dtype(X), _arg(gamma, "gamma", _F32, width, optional=True),
-                                 _arg(beta, "beta", _F32, width, optional=True), rows, width, float(eps),
-                                 _arg(Y, "Y", (X.dtype,), rows * width), _arg(mean, "mean", _F32, rows, optional=True),
-                                 _arg(rstd, "rstd", _F32, rows, optional=True), _stream(stream)), "svg2_layer_norm")
+    dev, f32, dtype = _device(), torch.float32, X.dtype
+    _check(lib().svg2_layer_norm(_ptr(X, "X", dtype, 0, dev), _dtype(X), _opt(gamma, "gamma", f32, width, dev),
+                                 _opt(beta, "beta", f32, width, dev), rows, width, float(eps),
+                                 _ptr(Y, "Y", dtype, rows * width, dev), _opt(mean, "mean", f32, rows, dev),
+                                 _opt(rstd, "rstd", f32, rows, dev), _stream(stream)), "svg2_layer_norm")
 
 
 def svg2_layer_norm_bwd_workspace_size(rows: int, width: int) -> int:
@@ -523,13 +557,14 @@ def svg2_layer_norm_bwd(X: torch.Tensor, dY: torch.Tensor, gamma: Optional[torch
                         dbeta: Optional[torch.Tensor], ws: torch.Tensor, stream=None):
     """Gradients of svg2_layer_norm from the mean and rstd it wrote."""
     rows, width = _rows(X, "X")
-    _one_device(X, dY, gamma, mean, rstd, dX, dgamma, dbeta, ws)
-    _check(lib().svg2_layer_norm_bwd(_arg(X, "X", _DATA, 0), _arg(dY, "dY", (X.dtype,), rows * width), _dtype(X),
-                                     _arg(gamma, "gamma", _F32, width, optional=True), _arg(mean, "mean", _F32, rows),
-                                     _arg(rstd, "rstd", _F32, rows), rows, width, _arg(dX, "dX", (X.dtype,), rows * width),
-                                     _arg(dgamma, "dgamma", _F32, width, optional=True),
-                                     _arg(dbeta, "dbeta", _F32, width, optional=True), _p(ws), _nbytes(ws),
-                                     _stream(stream)), "svg2_layer_norm_bwd")
+    dev, f32, dtype = _device(), torch.float32, X.dtype
+    n = rows * width
+    _check(lib().svg2_layer_norm_bwd(_ptr(X, "X", dtype, 0, dev), _ptr(dY, "dY", dtype, n, dev), _dtype(X),
+                                     _opt(gamma, "gamma", f32, width, dev), _ptr(mean, "mean", f32, rows, dev),
+                                     _ptr(rstd, "rstd", f32, rows, dev), rows, width, _ptr(dX, "dX", dtype, n, dev),
+                                     _opt(dgamma, "dgamma", f32, width, dev), _opt(dbeta, "dbeta", f32, width, dev),
+                                     _ptr(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream(stream)),
+           "svg2_layer_norm_bwd")
 
 
 def svg2_unpermute(Op: torch.Tensor, perm: torch.Tensor, O: torch.Tensor, stream=None):

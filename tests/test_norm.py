@@ -41,7 +41,7 @@ def forward_ref(X, gamma, beta, eps=EPS):
     e_mean = (DEEP + 2) * E * x.abs().mean(1, keepdim=True)
     e_c = e_mean + E * c.abs()
     e_var = (DEEP + 4) * E * var + 2 * (c.abs() * e_c).mean(1, keepdim=True) + (e_c ** 2).mean(1, keepdim=True)
-    rel = (0.5 * e_var / (var + eps) + 4 * E) * 1.1
+    rel = (0.5 * e_var / (var + eps) + 6 * E) * 1.1  # rsqrtf: 2 units in the last place = 4 E
     e_y = (rstd * e_c + xhat.abs() * rel) * ga.abs() + 3 * E * (xhat * ga).abs() + 2 * E * y.abs()
     return (y, e_y * 1.1 + half_step(X.dtype) * y.abs() + 1e-37), (mean[:, 0], e_mean[:, 0] + 1e-37), (rstd[:, 0], (rel * rstd)[:, 0])
 
