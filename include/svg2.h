@@ -242,7 +242,7 @@ SVG2_API int svg2_dense_attn(const void* Q, const void* K, const void* V, int B,
  *
  * svg2_dense_attn_lse / svg2_sparse_attn_lse are svg2_dense_attn / svg2_sparse_attn (same arguments,
  * workspace, errors and O, bit for bit) that also write
- *   (scale must be > 0 and finite here and in the gradient calls: SVG2_ERR_INVALID_ARG otherwise)
+ *   (scale must be finite and at least 1e-30 here and in the gradient calls: SVG2_ERR_INVALID_ARG otherwise)
  *   lse      float [B,H,N], out: lse_i = log sum_j exp(scale * q_i.k_j) over the row's keys, indexed by
  *            (permuted) row, whether perm_q is given or not; -inf for a row that keeps no key (O is 0). */
 SVG2_API int svg2_dense_attn_lse(const void* Q, const void* K, const void* V, int B, int H, int N, int d, float scale,

@@ -39,8 +39,9 @@ int to_status(cudaError_t e) { return e == cudaSuccess ? SVG2_OK : SVG2_ERR_CUDA
 
 bool finite_scale(float s) { return s == s && s != INFINITY && s != -INFINITY; }
 // The training calls: the softmax's maximum is taken before the scale, so a scale <= 0 would not be stable
-// (and would turn the -inf of masked columns into +inf or NaN).
-bool training_scale(float s) { return s > 0.f && s != INFINITY; }
+// (and would turn the -inf of masked columns into +inf or NaN); below 1e-30 a mask of the lowest bf16 would not
+// outweigh the scores any more.
+bool training_scale(float s) { return s >= 1e-30f && s != INFINITY; }
 
 bool valid_dtype(int dt) { return dt == SVG2_BF16 || dt == SVG2_F32; }
 

@@ -13,11 +13,10 @@
 //   query unit  Q, dO of 128 rows of one Q cluster stay; K, V of its kept clusters stream by.
 //               S = Q K^T, dP = dO V^T; dS goes back to TMEM as the A operand of dQ += dS K.
 // The streams are packed as in the forward: the kept clusters' rows back to back, so ragged cluster
-// edges cost no padding.  A tile is fetched by TMA in boxes of power-of-two heights, one run of boxes
-// per contiguous piece, the rows past the stream's end from outside the tensor (zero fill).
+// edges cost no padding; rows past the stream's end are zeros.
 //   warps 0-7   P and dS: TMEM lanes = resident rows, warps 0-3 the tile's columns 0-63, 4-7 64-127
 //   warp 8      TMEM allocator and MMA issuer
-//   warp 9      range table, then TMA producer (and the streamed queries' lse and delta by cp.async)
+//   warps 9-11  (9 alone when dense) range table, then the tiles' producers, and the streamed queries' lse, delta
 // P and dS are rounded to bf16 for the products (as P is in the forward); both stay float32 until then.
 // A row of dS sums to zero, so dQ does not depend on what all keys have in common; the rounded dS, with delta
 // from a bf16 O, sums to some r_i instead, and dQ would carry scale r_i times that common part, which
@@ -34,7 +33,7 @@ namespace svg2 {
 
 namespace {
 
-// 12 warps in three warpgroups: 8 for P and dS, then the MMA and producer warps (10 and 11 idle).
+// 12 warps in three warpgroups: 8 for P and dS, then the MMA and producer warps.
 constexpr int kBwdThreads = 384;
 // Register split after set-up (setmaxnreg): 256 x 176 + 128 x 152 = 64512 = 384 x 168, the launch's
 // allocation under __launch_bounds__(384, 1).  The one split in steps of 8 at which neither side spills
@@ -44,7 +43,6 @@ static_assert(256 * kBwdSoftmaxRegs + (kBwdThreads - 256) * kBwdOtherRegs <= kBw
               "register split");
 constexpr int kBwdMmaWarp = 8, kBwdProducerWarp = 9;
 constexpr int kBwdMaxRanges = 1024;
-constexpr int kBwdBoxes = 8;  // box heights 1, 2, ..., 128
 constexpr float kLog2e = 1.4426950408889634f;
 // Of every 16 column pairs, this many get 2^x from the cubic on the FMA pipe, the rest from the MUFU.
 constexpr int kBwdCubicPairs = 4;
@@ -54,7 +52,24 @@ constexpr uint32_t bwd_tile_bytes() { return 128u * D * 2u; }
 template <int D>
 constexpr uint32_t bwd_smem() {
   return 6 * bwd_tile_bytes<D>() + 1024 /*align*/ + 4 * 512 /*lse, delta of two stages*/ + 4096 /*range starts*/ +
-         4096 + 64 /*range offsets*/ + 2048 /*range segments*/ + 256 /*barriers*/;
+         4096 + 64 /*range offsets*/ + 2048 /*range segments*/ + 3 * 4096 /*segment operands*/ + 256 /*barriers*/;
+}
+// MULTI units: pairs that a row's own cluster does not keep get S = -3.4e38 from one more step of the S product,
+// 16 deep: A holds a one in the column of the row's cluster, B that column's penalty (0 or the lowest bf16) for the
+// streamed row.  A select per score instead made the key unit's softmax its longest part (8 x 12480 with 256
+// K clusters, every pair kept: 2.69 ms against 2.04).  Both operands [128, 16] are K-major without swizzle: 8 x 16-byte
+// blocks, the two of a row 128 bytes apart, 8-row groups 256 bytes apart.
+constexpr uint32_t kSegBytes = 4096;
+constexpr uint32_t kSegPenalty = 0xff7fu;  // bf16 -3.39e38
+__device__ __forceinline__ uint32_t seg_offset(int row) { return (row >> 3) * 256 + (row & 7) * 16; }
+// two bf16 per word, 16 values: the penalty where the bit of `keep` is clear
+__device__ __forceinline__ void store_seg(uint8_t* dst, uint32_t keep) {
+  uint32_t w[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    w[k] = ((keep >> (2 * k)) & 1u ? 0u : kSegPenalty) | ((keep >> (2 * k + 1)) & 1u ? 0u : kSegPenalty << 16);
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4*>(dst + 128) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 // Streams of up to this many tiles hand dS over as two bf16 numbers (its rounding, and the rest) and take one
@@ -64,8 +79,8 @@ constexpr uint32_t bwd_smem() {
 // the worst error of dQ and dK falls from 5.8e-3 and 3.0e-2 to 4.9e-3 and 2.1e-3 of their norms.
 constexpr int kBwdSplitTiles = 4;
 
-struct BwdMaps {  // [Q, K, V, dO][log2 box height], 64 columns wide, 128-byte swizzle
-  CUtensorMap m[4][kBwdBoxes];
+struct BwdMaps {  // Q, K, V, dO by [plane, row, column]: boxes of 128 rows x 64 columns, 128-byte swizzle
+  CUtensorMap m[4];
 };
 
 struct BwdArgs {
@@ -75,6 +90,7 @@ struct BwdArgs {
   const int32_t *perm_q, *perm_k;
   const float *neg_lse2, *neg_delta;                   // [BH, N] -lse log2(e), -delta, by permuted row
   const float* k_mean;                                 // [BH, D]
+  const __nv_bfloat16 *Q, *K, *V, *dO;                 // the tensors of the maps
   __nv_bfloat16 *dQ, *dK, *dV;
   int BH, N, nQ, nK, k_per_head, q_per_head;
   float scale;
@@ -193,47 +209,57 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
 // ------------------------------------------------------------------------------------------------
 constexpr int kBwdMaxSegments = 16;
 
-__device__ void write_units(const int32_t* off, int n, int N, int per_head, BwdUnit* out, int32_t* smem_off,
-                            DeviceStatus* st) {
-  __shared__ int32_t total;
-  for (int i = threadIdx.x; i <= n; i += blockDim.x) smem_off[i] = off[i];
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int count = 0;
-    BwdUnit open{0, 0, 0, 0};  // a unit that can still take rows
-    auto emit = [&](const BwdUnit& u) {
-      if (count < per_head) out[count] = u;
-      ++count;
-    };
-    int end = smem_off[0];
-    for (int j = 0; j < n; ++j) {
-      const int start0 = end;
-      end = smem_off[j + 1];
-      int start = start0, left = end - start0;
-      const bool ok = start >= 0 && left > 0 && start <= N - left;
-      SVG2_DEBUG_CHECK(ok || left == 0, st, kWherePlan, j, start);
-      if (!ok) continue;
-      if (open.nrows > 0 && open.row0 + open.nrows == start && j - open.cluster < kBwdMaxSegments) {
-        const int t = min(128 - open.nrows, left);
-        if ((left - t + 127) / 128 < (left + 127) / 128) {
-          open.nrows += t;
-          open.nseg = j - open.cluster + 1;
-          start += t;
-          left -= t;
-        }
-      }
-      if (left > 0) {
-        if (open.nrows > 0) emit(open);
-        for (; left >= 128; start += 128, left -= 128) emit(BwdUnit{j, start, 128, 1});
-        open = BwdUnit{j, start, left, 1};
+// Packs clusters [c0, c1) into units; `emit` takes them in order.  Returns their number.
+template <class Emit>
+__device__ __forceinline__ int pack_units(const int32_t* off, int c0, int c1, int N, Emit&& emit) {
+  int count = 0;
+  int first = 0, row0 = 0, rows = 0, last = 0;  // the unit that can still take rows (rows = 0: none)
+  int end = off[c0];
+  for (int j = c0; j < c1; ++j) {
+    int start = end;
+    end = off[j + 1];
+    int left = end - start;
+    if (start < 0 || left <= 0 || start > N - left) continue;  // empty, or malformed offsets
+    if (rows > 0 && row0 + rows == start && j - first < kBwdMaxSegments) {
+      const int t = min(128 - rows, left);
+      if (((left - t + 127) >> 7) < ((left + 127) >> 7)) {
+        rows += t;
+        last = j;
+        start += t;
+        left -= t;
       }
     }
-    if (open.nrows > 0) emit(open);
-    total = count;
+    if (left > 0) {
+      if (rows > 0) emit(count++, BwdUnit{first, row0, rows, last - first + 1});
+      for (; left >= 128; start += 128, left -= 128) emit(count++, BwdUnit{j, start, 128, 1});
+      first = last = j;
+      row0 = start;
+      rows = left;
+    }
   }
-  __syncthreads();
-  for (int s = total + threadIdx.x; s < per_head; s += blockDim.x) out[s] = BwdUnit{0, 0, 0, 0};
-  __syncthreads();
+  if (rows > 0) emit(count++, BwdUnit{first, row0, rows, last - first + 1});
+  return count;
+}
+
+// One warp packs a plane's clusters: each lane its own run of at least 16 (units do not cross runs, which
+// costs at most 31 units of a plane and keeps the scan short: a single thread took 70 us for 500 clusters).
+__device__ void write_units(const int32_t* off, int n, int N, int per_head, BwdUnit* out, DeviceStatus* st) {
+  const int lane = threadIdx.x & 31;
+  const int run = max(16, (n + 31) / 32);
+  const int c0 = min(n, lane * run), c1 = min(n, c0 + run);
+  for (int j = c0; j < c1; ++j) SVG2_DEBUG_CHECK(off[j] >= 0 && off[j + 1] >= off[j] && off[j + 1] <= N, st, kWherePlan, j, off[j]);
+  const int mine = pack_units(off, c0, c1, N, [](int, const BwdUnit&) {});
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const int base = incl - mine;
+  pack_units(off, c0, c1, N, [&](int i, const BwdUnit& u) {
+    if (base + i < per_head) out[base + i] = u;
+  });
+  for (int s = __shfl_sync(0xffffffffu, incl, 31) + lane; s < per_head; s += 32) out[s] = BwdUnit{0, 0, 0, 0};
 }
 
 __global__ void __launch_bounds__(512) bwd_plan_kernel(const int32_t* __restrict__ q_off,
@@ -244,15 +270,20 @@ __global__ void __launch_bounds__(512) bwd_plan_kernel(const int32_t* __restrict
                                                        BwdUnit* __restrict__ k_units, int k_per_head,
                                                        BwdUnit* __restrict__ q_units, int q_per_head,
                                                        DeviceStatus* st) {
-  extern __shared__ uint32_t bits[];  // [nK, WQ], then [16 warps][WK]
-  __shared__ int32_t offsets[kMaxClustersAssign + 1];
+  extern __shared__ uint32_t bits[];  // [nK, WQ], then [14 warps][WK]
+  __shared__ int32_t k_offsets[kMaxClustersAssign + 1], q_offsets[kMaxClustersAssign + 1];
   const int WQ = (nQ + 31) / 32, WK = (nK + 31) / 32;
   const int bh = blockIdx.x;
   for (int w = threadIdx.x; w < nK * WQ; w += blockDim.x) bits[w] = 0u;
+  for (int i = threadIdx.x; i <= nK; i += blockDim.x) k_offsets[i] = k_off[static_cast<size_t>(bh) * (nK + 1) + i];
+  for (int i = threadIdx.x; i <= nQ; i += blockDim.x) q_offsets[i] = q_off[static_cast<size_t>(bh) * (nQ + 1) + i];
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* mine = bits + nK * WQ + warp * WK;
-  for (int i = warp; i < nQ; i += static_cast<int>(blockDim.x >> 5)) {
+  // warps 14 and 15 write the units while the others turn the selection into bits
+  if (warp == 14) write_units(k_offsets, nK, N, k_per_head, k_units + static_cast<size_t>(bh) * k_per_head, st);
+  if (warp == 15) write_units(q_offsets, nQ, N, q_per_head, q_units + static_cast<size_t>(bh) * q_per_head, st);
+  for (int i = warp; i < nQ && warp < 14; i += 14) {
     const size_t row = static_cast<size_t>(bh) * nQ + i;
     for (int w = lane; w < WK; w += 32) mine[w] = 0u;
     __syncwarp();
@@ -275,10 +306,6 @@ __global__ void __launch_bounds__(512) bwd_plan_kernel(const int32_t* __restrict
   }
   __syncthreads();
   for (int w = threadIdx.x; w < nK * WQ; w += blockDim.x) keepers[static_cast<size_t>(bh) * nK * WQ + w] = bits[w];
-  write_units(k_off + static_cast<size_t>(bh) * (nK + 1), nK, N, k_per_head,
-              k_units + static_cast<size_t>(bh) * k_per_head, offsets, st);
-  write_units(q_off + static_cast<size_t>(bh) * (nQ + 1), nQ, N, q_per_head,
-              q_units + static_cast<size_t>(bh) * q_per_head, offsets, st);
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -295,10 +322,10 @@ struct BwdTmem {
   static constexpr uint32_t dp = 256, acc2 = 384;     // acc2: dK | dQ
 };
 
-template <int D, bool KV, bool SPLIT, bool MULTI>
+template <int D, bool DENSE, bool KV, bool SPLIT, bool MULTI>
 __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, const BwdUnit un, const int bh,
                                          uint8_t* smem, BwdBars* bars, float* stats, const int32_t* r_start,
-                                         const int32_t* r_cum, const uint16_t* r_seg, float* scratch, const long long wb) {
+                                         const int32_t* r_cum, const uint16_t* r_seg, uint8_t* seg_s, float* scratch, const long long wb) {
   constexpr uint32_t kTile = bwd_tile_bytes<D>();
   constexpr int kHalves = D / 64;   // 128-byte swizzle atoms across a row
   constexpr int kSteps = D / 16;    // instructions of one S or dP product
@@ -307,7 +334,6 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
   const uint32_t tmem = bars->tmem_base;
   const int L = bars->L;
   const int T = (L + 127) / 128;
-  const bool dense = a.q_off == nullptr;
   DeviceStatus* st = a.st;
   const uint32_t r1 = smem_u32(smem), r2 = r1 + kTile, t1 = r1 + 2 * kTile, t2 = r1 + 4 * kTile;
 
@@ -316,13 +342,16 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       const uint32_t id_s = idesc_bf16_f32(128, 128, 0);  // both operands K-major
       const uint32_t id_o = idesc_bf16_f32(128, D, 1);    // B = a streamed tile read row-major (MN-major)
       // D[slot] = R x T^T, contraction over d
-      auto product = [&](uint32_t d_tmem, uint32_t ra, uint32_t tb) {
+      auto product = [&](uint32_t d_tmem, uint32_t ra, uint32_t tb, int seg_stage) {
         const uint64_t da = sdesc_sw128(ra, 16, 1024), db = sdesc_sw128(tb, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
           const uint64_t off = static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
           mma_ss(d_tmem, da + off, db + off, id_s, ks > 0 ? 1u : 0u);
         }
+        if (MULTI && seg_stage >= 0)
+          mma_ss(d_tmem, sdesc_plain(smem_u32(seg_s), 128, 256), sdesc_plain(smem_u32(seg_s) + (1 + seg_stage) * kSegBytes, 128, 256),
+                 id_s, 1u);
       };
       // acc (+)= X T with X (P or dS, bf16) in TMEM, contraction over the tile's 128 rows
       auto accumulate = [&](uint32_t acc, uint32_t x, uint32_t tb, bool add) {
@@ -335,16 +364,21 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       auto wait = [&](uint64_t* bar, int phase) {
         return mbar_wait(smem_u32(bar), phase & 1, st, kWhereAttnBwdMma, wb);
       };
-      bool ok = wait(&bars->res_full, 0) && wait(&bars->t1_full[0], 0);
+      auto wait_tile = [&](uint64_t* bar, int phase) {
+        const bool landed = wait(bar, phase);
+        if (!DENSE) fence_proxy_async_smem();  // rows gathered by cp.async (generic proxy)
+        return landed;
+      };
+      bool ok = wait(&bars->res_full, 0) && wait_tile(&bars->t1_full[0], 0);
       if (ok) {
         tc_fence_after();
-        product(tmem, r1, t1);
+        product(tmem, r1, t1, 0);
         mma_commit(smem_u32(&bars->s_full[0]));
-        ok = wait(&bars->t2_full[0], 0);
+        ok = wait_tile(&bars->t2_full[0], 0);
       }
       if (ok) {
         tc_fence_after();
-        product(tmem + Tm::dp, r2, t2);
+        product(tmem + Tm::dp, r2, t2, -1);
         mma_commit(smem_u32(&bars->dp_full));
         if (!KV) mma_commit(smem_u32(&bars->t2_empty[0]));
       }
@@ -361,10 +395,10 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         if (more) {
           // key unit: the products run in issue order, so S(j+1) overwrites P(j) only after dV has read it;
           // query unit: the other slot, whose S(j-1) was read before dS(j-1) was handed over
-          ok = wait(&bars->t1_full[ng], (j + 1) >> 1);
+          ok = wait_tile(&bars->t1_full[ng], (j + 1) >> 1);
           if (!ok) break;
           tc_fence_after();
-          product(tmem + (KV ? 0u : ng * Tm::s1), r1, t1 + ng * kTile);
+          product(tmem + (KV ? 0u : ng * Tm::s1), r1, t1 + ng * kTile, ng);
           mma_commit(smem_u32(&bars->s_full[KV ? 0 : ng]));
         }
         ok = wait(&bars->ds_full, j);
@@ -374,10 +408,10 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         if constexpr (SPLIT) accumulate(tmem + Tm::acc2, tmem + Tm::dp + 32, t1 + sg * kTile, true);
         mma_commit(smem_u32(&bars->t1_empty[sg]));
         if (more) {
-          ok = wait(&bars->t2_full[ng], (j + 1) >> 1);
+          ok = wait_tile(&bars->t2_full[ng], (j + 1) >> 1);
           if (!ok) break;
           tc_fence_after();
-          product(tmem + Tm::dp, r2, t2 + ng * kTile);
+          product(tmem + Tm::dp, r2, t2 + ng * kTile, -1);
           mma_commit(smem_u32(&bars->dp_full));
           if (!KV) mma_commit(smem_u32(&bars->t2_empty[ng]));
         }
@@ -386,85 +420,131 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       mma_commit(smem_u32(&bars->mma_done));
       mbar_wait(smem_u32(&bars->mma_done), 0, nullptr, kWhereAttnBwdMma, kWaitBudgetCycles / 8);
     }
-  } else if (warp == kBwdProducerWarp) {
-    const bool leader = elect_one();
-    const CUtensorMap* m1 = maps.m[KV ? 0 : 1];
-    const CUtensorMap* m2 = maps.m[KV ? 3 : 2];
+  } else if (warp == kBwdProducerWarp || (!DENSE && warp > kBwdProducerWarp)) {
+    // ---------------- resident and streamed tiles ----------------
+    // A tile that is one contiguous piece comes by TMA: every dense tile (its rows past the plane's end are
+    // zero-filled), and a sparse one inside a range.  A sparse tile of several pieces is gathered with
+    // 16-byte cp.async copies by warps 9 to 11 (rows 0-47, 48-87, 88-127): as TMA boxes, one run per piece,
+    // the single issuing thread took 1.6 times the tile's products at 49 rows per cluster.
+    const int pw = warp - kBwdProducerWarp;
+    const bool leader = pw == 0 && elect_one();
+    const CUtensorMap* m1 = &maps.m[KV ? 0 : 1];
+    const CUtensorMap* m2 = &maps.m[KV ? 3 : 2];
     if (leader && T > 0) {
       const uint32_t bar = smem_u32(&bars->res_full);
       mbar_arrive_expect_tx(bar, 2 * kTile);
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        tma_load_3d(r1 + h * 16384, &maps.m[KV ? 1 : 0][7], h * 64, un.row0, bh, bar);
-        tma_load_3d(r2 + h * 16384, &maps.m[KV ? 2 : 3][7], h * 64, un.row0, bh, bar);
+        tma_load_3d(r1 + h * 16384, &maps.m[KV ? 1 : 0], h * 64, un.row0, bh, bar);
+        tma_load_3d(r2 + h * 16384, &maps.m[KV ? 2 : 3], h * 64, un.row0, bh, bar);
       }
     }
-    // rows [at, at + n) of a tile <- rows [row, row + n) of the plane (row = N: zeros), in boxes
-    auto fetch = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int at, int n, int row) {
-      while (n > 0) {
-        const int b = 31 - __clz(n);
+    auto tma_tile = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int row) {
+      mbar_arrive_expect_tx(bar, kTile);
 #pragma unroll
-        for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * 16384 + at * 128, &m[b], h * 64, row, bh, bar);
-        at += 1 << b;
-        n -= 1 << b;
-        if (row < a.N) row += 1 << b;
-      }
+      for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * 16384, m, h * 64, row, bh, bar);
     };
-    // calls f(first tile row, rows, first plane row) for the pieces of tile j; e: the range that holds its first row
-    auto pieces = [&](int j, int& e, auto&& f) {
-      int p = j * 128, at = 0;
-      if (dense) {  // one box: its rows past the plane's end are zero-filled
-        f(0, 128, p);
-        return;
-      }
-      while (at < 128 && p < L) {
-        while (r_cum[e + 1] <= p) ++e;
-        const int n = min(r_cum[e + 1] - p, 128 - at);
-        f(at, n, r_start[e] + (p - r_cum[e]));
-        at += n;
-        p += n;
-      }
-      if (at < 128) f(at, 128 - at, a.N);
-    };
-    int e1 = 0, e2 = 0;
+    const size_t plane = static_cast<size_t>(bh) * a.N;
+    const float* nl = a.neg_lse2 + plane;
+    const float* nd = a.neg_delta + plane;
     int n1 = 0, n2 = 0;  // tiles requested of each streamed operand
     bool ok = true;
-    const float* nl = a.neg_lse2 + static_cast<size_t>(bh) * a.N;
-    const float* nd = a.neg_delta + static_cast<size_t>(bh) * a.N;
-    for (int j = 0; j < T; ++j) {
-      const int sg = j & 1;
-      const uint32_t b1 = smem_u32(&bars->t1_full[sg]), b2 = smem_u32(&bars->t2_full[sg]);
-      if (j >= 2) {
-        ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&bars->t1_empty[sg]), ((j >> 1) - 1) & 1, st,
-                                                     kWhereAttnBwdProducer, 32, wb));
+    auto wait_empty = [&](uint64_t* bar, int j) {
+      return j < 2 || __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(bar), ((j >> 1) - 1) & 1, st,
+                                                              kWhereAttnBwdProducer, 32, wb));
+    };
+    // -lse log2(e) and -delta of plane row `row` into column c of the stage (row < 0: zeros)
+    auto stat = [&](int sg, int c, int row) {
+      const uint32_t dst = smem_u32(stats + sg * 256 + c);
+      cp_async4(dst, nl + max(row, 0), row >= 0 ? 4u : 0u);
+      cp_async4(dst + 512, nd + max(row, 0), row >= 0 ? 4u : 0u);
+    };
+    if constexpr (DENSE) {
+      for (int j = 0; j < T; ++j) {
+        const int sg = j & 1;
+        const uint32_t b1 = smem_u32(&bars->t1_full[sg]);
+        ok = wait_empty(&bars->t1_empty[sg], j);
         if (!ok) break;
-      }
-      if (leader) mbar_arrive_expect_tx(b1, kTile);
-      __syncwarp();
-      pieces(j, e1, [&](int at, int n, int row) {
-        if (leader) fetch(m1, t1 + sg * kTile, b1, at, n, row);
+        if (leader) tma_tile(m1, t1 + sg * kTile, b1, j * 128);
         if constexpr (KV) {
-          for (int x = lane; x < n; x += 32) {
-            const bool in = row + x < a.N;  // past the stream's end: 0, and the column is masked
-            const uint32_t dst = smem_u32(stats + sg * 256 + at + x);
-            cp_async4(dst, nl + (in ? row + x : 0), in ? 4u : 0u);
-            cp_async4(dst + 512, nd + (in ? row + x : 0), in ? 4u : 0u);
-          }
+#pragma unroll
+          for (int c = lane; c < 128; c += 32) stat(sg, c, j * 128 + c < a.N ? j * 128 + c : -1);
+          cp_async_mbar_arrive(b1);
         }
-      });
-      if constexpr (KV) cp_async_mbar_arrive(b1);
-      n1 = j + 1;
-      if (j >= 2) {
-        ok = __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(&bars->t2_empty[sg]), ((j >> 1) - 1) & 1, st,
-                                                     kWhereAttnBwdProducer, 32, wb));
+        n1 = j + 1;
+        ok = wait_empty(&bars->t2_empty[sg], j);
         if (!ok) break;
+        if (leader) tma_tile(m2, t2 + sg * kTile, smem_u32(&bars->t2_full[sg]), j * 128);
+        n2 = j + 1;
       }
-      if (leader) mbar_arrive_expect_tx(b2, kTile);
-      __syncwarp();
-      pieces(j, e2, [&](int at, int n, int row) {
-        if (leader) fetch(m2, t2 + sg * kTile, b2, at, n, row);
-      });
-      n2 = j + 1;
+    } else {
+      constexpr int CPR = D / 8;           // 16-byte chunks per row
+      constexpr int RPI = 32 / CPR;        // rows per warp instruction
+      constexpr int kIters = 48 / RPI;     // at most this many instructions per tile and operand
+      constexpr int kPeriod = 8 / RPI;     // the row's place in its 8-row swizzle group repeats this often
+      const int wr0 = pw == 0 ? 0 : (pw == 1 ? 48 : 88), nrw = pw == 0 ? 48 : 40;
+      const int chunk = lane % CPR, sub = lane / CPR;
+      uint32_t xo[kPeriod];  // this thread's byte offset within a tile, less it * RPI * 128
+#pragma unroll
+      for (int k = 0; k < kPeriod; ++k)
+        xo[k] = (chunk >> 3) * 16384 + (wr0 + sub) * 128 + (((chunk & 7) ^ ((k * RPI + sub) & 7)) << 4);
+      const __nv_bfloat16* s1 = (KV ? a.Q : a.K) + plane * D + chunk * 8;
+      const __nv_bfloat16* s2 = (KV ? a.dO : a.V) + plane * D + chunk * 8;
+      int e0 = 0, e1 = 0, et = 0;  // ranges of this lane's two stream positions and of the tile's first
+      auto src_row = [&](int p, int& e) {
+        if (p >= L) return -1;
+        while (r_cum[e + 1] <= p) ++e;
+        return r_start[e] + (p - r_cum[e]);
+      };
+      for (int j = 0; j < T; ++j) {
+        const int sg = j & 1;
+        const uint32_t b1 = smem_u32(&bars->t1_full[sg]), b2 = smem_u32(&bars->t2_full[sg]);
+        const int g0 = src_row(j * 128 + wr0 + lane, e0), g1 = src_row(j * 128 + wr0 + 32 + lane, e1);
+        while (r_cum[et + 1] <= j * 128) ++et;
+        const bool whole = r_cum[et + 1] >= j * 128 + 128;
+        const int first = r_start[et] + (j * 128 - r_cum[et]);
+        auto gather = [&](uint32_t dst, const __nv_bfloat16* src) {
+#pragma unroll
+          for (int it = 0; it < kIters; ++it) {
+            if (it * RPI >= nrw) break;
+            const int g = __shfl_sync(0xffffffffu, it * RPI < 32 ? g0 : g1, (it * RPI + sub) & 31);
+            cp_async16_zfill(dst + xo[it % kPeriod] + it * RPI * 128, src + static_cast<size_t>(max(g, 0)) * D, g >= 0);
+          }
+        };
+        ok = wait_empty(&bars->t1_empty[sg], j);
+        if (!ok) break;
+        if (whole) {
+          if (leader) tma_tile(m1, t1 + sg * kTile, b1, first);
+        } else {
+          if (leader) mbar_arrive(b1);
+          gather(t1 + sg * kTile, s1);
+        }
+        if constexpr (KV) {
+          stat(sg, wr0 + lane, g0);
+          if (32 + lane < nrw) stat(sg, wr0 + 32 + lane, g1);
+        }
+        cp_async_mbar_arrive(b1);
+        if constexpr (MULTI) {  // (plain stores: an arrival of their own orders them)
+          auto segs = [&](int c, int g, int e) {
+            if (g >= 0) store_seg(seg_s + (1 + sg) * kSegBytes + seg_offset(c), r_seg[e]);
+          };
+          segs(wr0 + lane, g0, e0);
+          if (32 + lane < nrw) segs(wr0 + 32 + lane, g1, e1);
+          fence_proxy_async_smem();
+        }
+        mbar_arrive(b1);
+        n1 = j + 1;
+        ok = wait_empty(&bars->t2_empty[sg], j);
+        if (!ok) break;
+        if (whole) {
+          if (leader) tma_tile(m2, t2 + sg * kTile, b2, first);
+        } else {
+          if (leader) mbar_arrive(b2);
+          gather(t2 + sg * kTile, s2);
+        }
+        cp_async_mbar_arrive(b2);
+        n2 = j + 1;
+      }
     }
     // Every copy has landed before the CTA leaves, also when some agent gave up: the last phase of each
     // stage's barrier is awaited here (older phases are complete, or the stage would not have been reused).
@@ -492,16 +572,10 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       nl_row = a.neg_lse2[plane + un.row0 + row];
       nd_row = a.neg_delta[plane + un.row0 + row];
     }
-    // MULTI: this row's cluster among the unit's, and the range that holds this half's first column
-    int seg = 0, range = 0;
-    if constexpr (MULTI) {
-      const int32_t* off = KV ? a.k_off + static_cast<size_t>(bh) * (a.nK + 1) : a.q_off + static_cast<size_t>(bh) * (a.nQ + 1);
-      while (seg + 1 < un.nseg && off[un.cluster + seg + 1] <= un.row0 + row) ++seg;
-    }
     auto wait = [&](uint64_t* bar, int phase) {
       return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, st, kWhereAttnBwdSoftmax, wb));
     };
-    const bool exact_delta = SPLIT && T == 1 && (!KV || (dense && a.N <= 128));
+    const bool exact_delta = SPLIT && T == 1 && (!KV || (DENSE && a.N <= 128));
     float2 r_sum = make_float2(0.f, 0.f);  // query unit: this half's sum of the row's rounded dS
     bool ok = true;
     for (int j = 0; j < T; ++j) {
@@ -523,22 +597,6 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
 #pragma unroll
         for (int e = 0; e < 64; ++e)
           if (e >= valid) sv[e] = __float_as_uint(-INFINITY);
-      }
-      if constexpr (MULTI) {  // pairs that this row's cluster does not keep: P = 0
-        const int p0 = j * 128 + half * 64;
-        unsigned long long drop = 0ull;
-        if (p0 < L) {
-          while (r_cum[range + 1] <= p0) ++range;
-          for (int e = range, at = 0; at < 64 && p0 + at < L; ++e) {
-            const int n = min(r_cum[e + 1] - (p0 + at), 64 - at);
-            if (!((r_seg[e] >> seg) & 1)) drop |= (n == 64 ? ~0ull : (1ull << n) - 1ull) << at;
-            at += n;
-          }
-        }
-        const uint32_t d0 = static_cast<uint32_t>(drop), d1 = static_cast<uint32_t>(drop >> 32);
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (((e < 32 ? d0 : d1) >> (e & 31)) & 1u) sv[e] = __float_as_uint(-INFINITY);
       }
       // P = 2^(s log2(e) - lse log2(e))
       float2 p[32];
@@ -787,14 +845,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   int32_t* r_start = reinterpret_cast<int32_t*>(stats + 512);
   int32_t* r_cum = r_start + kBwdMaxRanges;  // kBwdMaxRanges + 1 entries
   uint16_t* r_seg = reinterpret_cast<uint16_t*>(r_cum + kBwdMaxRanges + 16);
-  BwdBars* bars = reinterpret_cast<BwdBars*>(r_seg + kBwdMaxRanges);
+  uint8_t* seg_s = reinterpret_cast<uint8_t*>(r_seg + kBwdMaxRanges);  // this unit's rows, then two streamed tiles'
+  BwdBars* bars = reinterpret_cast<BwdBars*>(seg_s + 3 * kSegBytes);
   const int warp = threadIdx.x >> 5;
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->res_full), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&bars->t1_full[i]), kv ? 33 : 1);  // the bytes, and each producer lane's small copies
-      mbar_init(smem_u32(&bars->t2_full[i]), 1);
+      // the TMA bytes (or the leader's arrival), each producer lane's own copies and, when sparse, its plain stores
+      mbar_init(smem_u32(&bars->t1_full[i]), dense ? (kv ? 33 : 1) : 193);
+      mbar_init(smem_u32(&bars->t2_full[i]), dense ? 1 : 97);
       mbar_init(smem_u32(&bars->t1_empty[i]), 1);
       mbar_init(smem_u32(&bars->t2_empty[i]), 1);
       mbar_init(smem_u32(&bars->s_full[i]), 1);
@@ -810,6 +870,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
   }
+  if (!dense && warp < 4) {  // this row's cluster among the unit's
+    const int row = threadIdx.x;
+    const int32_t* off = kv ? a.k_off + static_cast<size_t>(bh) * (a.nK + 1) : a.q_off + static_cast<size_t>(bh) * (a.nQ + 1);
+    int seg = 0;
+    while (seg + 1 < un.nseg && off[un.cluster + seg + 1] <= un.row0 + row) ++seg;
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = seg == 2 * k ? 0x3f80u : (seg == 2 * k + 1 ? 0x3f800000u : 0u);
+    *reinterpret_cast<uint4*>(seg_s + seg_offset(row)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(seg_s + seg_offset(row) + 128) = make_uint4(w[4], w[5], w[6], w[7]);
+    fence_proxy_async_smem();
+  }
   if (warp == kBwdProducerWarp) {
     if (!dense) build_ranges(a, un, bh, kv, r_start, r_cum, r_seg, bars);
     else if ((threadIdx.x & 31) == 0) bars->L = a.N;
@@ -821,7 +893,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwdSoftmaxRegs) : "memory");
   float* scratch = reinterpret_cast<float*>(r_start);
 #define SVG2_BWD_UNIT(KV, SPLIT, MULTI) \
-  bwd_unit<D, KV, SPLIT, MULTI>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, r_seg, scratch, wb)
+  bwd_unit<D, dense, KV, SPLIT, MULTI>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, r_seg, seg_s, scratch, wb)
   if constexpr (dense) {
     constexpr bool kShort = KIND == BwdKind::kDenseShort;
     if (kv) SVG2_BWD_UNIT(true, kShort, false);
@@ -898,8 +970,11 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   alignas(64) BwdMaps maps;
   const void* base[4] = {in.Q, in.K, in.V, in.perm_q != nullptr ? sc.dOp : in.dO};
   for (int t = 0; t < 4 && e == cudaSuccess; ++t)
-    for (int b = dense ? kBwdBoxes - 1 : 0; b < kBwdBoxes && e == cudaSuccess; ++b)
-      e = make_tmap_bf16_3d(&maps.m[t][b], base[t], D, N, BH, D * 2, static_cast<uint64_t>(N) * D * 2, 1u << b);
+    e = make_tmap_bf16_3d(&maps.m[t], base[t], D, N, BH, D * 2, static_cast<uint64_t>(N) * D * 2, 128);
+  a.Q = static_cast<const __nv_bfloat16*>(base[0]);
+  a.K = static_cast<const __nv_bfloat16*>(base[1]);
+  a.V = static_cast<const __nv_bfloat16*>(base[2]);
+  a.dO = static_cast<const __nv_bfloat16*>(base[3]);
   if (e != cudaSuccess) return e;
   auto* kernel = !dense ? attn_bwd_kernel<D, BwdKind::kSparse>
                         : (N <= kBwdSplitTiles * 128 ? attn_bwd_kernel<D, BwdKind::kDenseShort>

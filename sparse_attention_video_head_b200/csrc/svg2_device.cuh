@@ -287,6 +287,17 @@ __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t start, uint32_t lbo, ui
   return d;
 }
 
+// The same without swizzle: blocks of 8 rows x 16 bytes; for a K-major operand lbo is the distance of
+// neighbouring blocks along K, sbo that of neighbouring 8-row groups.
+__device__ __forceinline__ uint64_t sdesc_plain(uint32_t start, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((start >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  return d;
+}
+
 // ------------------------------------------------------------------------------------------------
 // TMEM <-> registers (32 lanes x 32-bit, warp-wide; lane quarter = warp id % 4)
 // ------------------------------------------------------------------------------------------------
