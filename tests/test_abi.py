@@ -256,3 +256,94 @@ def test_noalloc_checks_sizes_before_any_cuda_call(L):
     assert call(nQ=1001) == INVALID            # more clusters than tokens
     assert call(Q=None) == INVALID
     assert call(Q=ctypes.c_void_p(0x10008)) == INVALID
+
+
+def _named(L, fn, defaults, order):
+    return lambda **kw: getattr(L, fn)(*[dict(defaults, **kw)[n] for n in order])
+
+
+def test_attention_training_calls_reject_bad_arguments(L):
+    from sparse_attention_video_head_b200 import svg2
+    out = ctypes.c_size_t(0)
+    assert L.svg2_dense_attn_bwd_workspace_size(1, 2, 1000, 128, ctypes.byref(out)) == OK
+    assert out.value >= svg2.svg2_dense_attn_workspace_size(1, 2, 1000, 128)   # serves the forward too
+    assert L.svg2_dense_attn_bwd_workspace_size(1, 2, 1000, 128, None) == INVALID
+    assert L.svg2_dense_attn_bwd_workspace_size(1, 2, 1000, 96, ctypes.byref(out)) == UNSUPPORTED
+    assert L.svg2_dense_attn_bwd_workspace_size(1, 65536, 4, 64, ctypes.byref(out)) == UNSUPPORTED
+    assert L.svg2_sparse_attn_bwd_workspace_size(1, 2, 1000, 128, 4, 8, ctypes.byref(out)) == OK and out.value > 1000 * 512
+    assert L.svg2_sparse_attn_bwd_workspace_size(1, 2, 1000, 128, 4, 1001, ctypes.byref(out)) == INVALID
+    assert L.svg2_sparse_attn_bwd_workspace_size(1, 2, 5000, 128, 1025, 4, ctypes.byref(out)) == UNSUPPORTED
+    P = lambda i: ctypes.c_void_p(0x10000 * (i + 1))  # noqa: E731
+    bad = ctypes.c_void_p(0x10008)
+    F = ctypes.c_float
+    big = 1 << 34
+    t = {n: P(i) for i, n in enumerate(("Q", "K", "V", "O", "dO", "dQ", "dK", "dV", "lse", "qo", "ko", "sc", "si"))}
+    size = dict(B=1, H=2, N=1000, d=128, s=F(0.1), nQ=4, nK=8, pq=None, pk=None, ws=P(20), wsb=big, st=None)
+    dense_f = _named(L, "svg2_dense_attn_lse", {**t, **size},
+                     ("Q", "K", "V", "B", "H", "N", "d", "s", "O", "lse", "ws", "wsb", "st"))
+    sparse_f = _named(L, "svg2_sparse_attn_lse", {**t, **size},
+                      ("Q", "K", "V", "qo", "ko", "sc", "si", "B", "H", "N", "d", "nQ", "nK", "s", "pq", "O", "lse", "ws",
+                       "wsb", "st"))
+    dense_b = _named(L, "svg2_dense_attn_bwd", {**t, **size},
+                     ("Q", "K", "V", "O", "lse", "dO", "B", "H", "N", "d", "s", "dQ", "dK", "dV", "ws", "wsb", "st"))
+    sparse_b = _named(L, "svg2_sparse_attn_bwd", {**t, **size},
+                      ("Q", "K", "V", "O", "lse", "dO", "qo", "ko", "sc", "si", "B", "H", "N", "d", "nQ", "nK", "s", "pq",
+                       "pk", "dQ", "dK", "dV", "ws", "wsb", "st"))
+    for call in (dense_f, sparse_f, dense_b, sparse_b):
+        for n in ("Q", "K", "V", "O", "lse"):
+            assert call(**{n: None}) == INVALID, n
+        for n in ("Q", "K", "V", "O"):
+            assert call(**{n: bad}) == INVALID, n              # not 16-byte aligned
+        assert call(lse=ctypes.c_void_p(0x10002)) == INVALID
+        for s in (0.0, -0.1, float("nan"), float("inf"), 1e-31):
+            assert call(s=F(s)) == INVALID, s
+        assert call(d=96) == UNSUPPORTED
+        assert call(N=0) == INVALID
+        assert call(ws=None) == WORKSPACE
+        assert call(ws=ctypes.c_void_p(0x10010)) == WORKSPACE
+        assert call(wsb=64) == WORKSPACE
+    for call in (dense_b, sparse_b):
+        for n in ("dO", "dQ", "dK", "dV"):
+            assert call(**{n: None}) == INVALID
+            assert call(**{n: bad}) == INVALID
+        assert call(dQ=t["Q"]) == INVALID                       # an output over an input, or over another output
+        assert call(dV=t["dO"]) == INVALID
+        assert call(dK=t["dV"]) == INVALID
+    for call in (sparse_f, sparse_b):
+        for n in ("qo", "ko", "sc", "si"):
+            assert call(**{n: None}) == INVALID
+        assert call(nQ=0) == INVALID
+        assert call(nK=1025, N=2000) == UNSUPPORTED
+
+
+def test_layer_norm_rejects_bad_arguments(L):
+    out = ctypes.c_size_t(0)
+    size = lambda r, w: L.svg2_layer_norm_bwd_workspace_size(r, w, ctypes.byref(out))  # noqa: E731
+    assert size(1, 1) == OK and size((1 << 31) - 1, 8192) == OK
+    assert size(0, 64) == INVALID and size(4, 0) == INVALID
+    assert size(1 << 31, 64) == UNSUPPORTED and size(4, 8193) == UNSUPPORTED
+    assert L.svg2_layer_norm_bwd_workspace_size(4, 64, None) == INVALID
+    F = ctypes.c_float
+    d = dict(X=FAKE, dY=ctypes.c_void_p(0x20000), dt=0, g=None, b=None, m=FAKE, r=FAKE, R=10, W=64, e=F(1e-6), Y=FAKE,
+             dg=None, db=None, ws=FAKE, wsb=1 << 30, st=None)
+    fwd = _named(L, "svg2_layer_norm", d, ("X", "dt", "g", "b", "R", "W", "e", "Y", "m", "r", "st"))
+    bwd = _named(L, "svg2_layer_norm_bwd", d, ("X", "dY", "dt", "g", "m", "r", "R", "W", "Y", "dg", "db", "ws", "wsb", "st"))
+    odd = ctypes.c_void_p(0x10001)
+    for call in (fwd, bwd):
+        assert call(X=None) == INVALID
+        assert call(Y=None) == INVALID
+        assert call(X=odd) == INVALID
+        assert call(g=ctypes.c_void_p(0x10002)) == INVALID
+        assert call(dt=5) == INVALID
+        assert call(R=0) == INVALID
+        assert call(W=0) == INVALID
+        assert call(W=8193) == UNSUPPORTED
+        assert call(R=1 << 31) == UNSUPPORTED
+    for e in (-1e-6, float("nan"), float("inf")):
+        assert fwd(e=F(e)) == INVALID
+    assert bwd(dY=None) == INVALID
+    assert bwd(m=None) == INVALID
+    assert bwd(r=None) == INVALID
+    assert bwd(dg=FAKE, db=FAKE) == INVALID
+    assert bwd(ws=None) == WORKSPACE
+    assert bwd(wsb=256) == WORKSPACE

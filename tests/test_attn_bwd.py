@@ -17,7 +17,13 @@ from tests.gpu_helpers import require_gpu
 U = 2.0 ** -8
 
 
-def formulas(q, k, v, do, scale, keep=None):
+def mean_key(k):
+    S = min(512, k.shape[0])
+    x = k[torch.arange(S, device=k.device) * k.shape[0] // S].double()
+    return torch.where(x.isfinite(), x, 0.0).mean(0)
+
+
+def formulas(q, k, v, do, scale, keep=None, c=None):
     """Float64 outputs and their error bounds for one plane [N, d]; keep [N, N]: the kept pairs."""
     q, k, v, do = (x.double() for x in (q, k, v, do))
     d = q.shape[1]
@@ -37,8 +43,7 @@ def formulas(q, k, v, do, scale, keep=None):
     pv = p @ v.abs()
     e_o = (U + ep.amax(1, keepdim=True)) * pv + U * o.abs()
     e_delta = (do.abs() * e_o).sum(1, keepdim=True) + d * 2.0 ** -23 * (do.abs() * o.abs()).sum(1, keepdim=True)
-    S = min(512, k.shape[0])
-    c = k[torch.arange(S, device=k.device) * k.shape[0] // S].mean(0)
+    c = mean_key(k) if c is None else c
     e_dp = d * 2.0 ** -23 * (do.abs() @ v.abs().T)
     e_ds = (U + 2 * ep) * ds.abs() + p * (e_delta + e_dp) * (1 + U)
     tol = {"O": e_o, "dV": ((U + ep) * p).T @ do.abs() + U * out["dV"].abs(),
@@ -194,3 +199,277 @@ def test_sparse_gradients(B, H, N, d, nQ, nK, density, kw, perms):
             for n in ref:
                 x = got[n][b, h] if n == "lse" else by_row(got[n], pk if n in ("dK", "dV") else pq, b, h)
                 check(x, ref[n], tol[n], (n, b, h), norm=n != "lse" and N >= 300)
+
+
+def same(a, b):
+    return all(torch.equal(a[n], b[n]) for n in a)
+
+
+@pytest.mark.gpu
+def test_forward_is_the_plain_call_bit_for_bit_and_runs_repeat():
+    svg2 = require_gpu()
+    g = gen(8)
+    Q, K, V, dO = (randn(g, 1, 3, 901, 128) for _ in range(4))
+    got = dense_step(svg2, Q, K, V, dO, 0.1)
+    O = torch.empty_like(Q)
+    svg2.svg2_dense_attn(Q, K, V, 0.1, O, svg2.dense_workspace(1, 3, 901, 128))
+    assert torch.equal(O, got["O"])
+    pl = plan(3, 1, 3, 901, 9, 30, 0.5)
+    one = sparse_step(svg2, pl, Q, K, V, dO, 0.1)
+    svg2.svg2_sparse_attn(Q, K, V, *(pl[n] for n in ("q_off", "k_off", "sel_count", "sel_idx")), 0.1, O,
+                          svg2.workspace(1, 3, 901, 128, 9, 30), perm_q=pl["perm_q"])
+    assert torch.equal(O, one["O"])
+    for _ in range(3):
+        assert same(dense_step(svg2, Q, K, V, dO, 0.1), got)
+        assert same(sparse_step(svg2, pl, Q, K, V, dO, 0.1), one)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_planes_do_not_leak(d):
+    """Rows past a plane's end belong to the next plane: NaN and infinity there reach nothing."""
+    svg2 = require_gpu()
+    g = gen(d)
+    Q, K, V, dO = (randn(g, 1, 3, 321, d) for _ in range(4))
+    ref = dense_step(svg2, Q, K, V, dO, 0.1)
+    pl = plan(4, 1, 3, 321, 5, 9, 0.5)
+    sref = sparse_step(svg2, pl, Q, K, V, dO, 0.1)
+    for t, bad in ((Q, torch.nan), (K, torch.inf), (V, torch.nan), (dO, -torch.inf)):
+        t[:, 2] = bad
+    got = dense_step(svg2, Q, K, V, dO, 0.1)
+    sgot = sparse_step(svg2, pl, Q, K, V, dO, 0.1)
+    for n in ref:
+        assert torch.equal(got[n][:, :2], ref[n][:, :2]) and torch.equal(sgot[n][:, :2], sref[n][:, :2]), n
+
+
+@pytest.mark.gpu
+def test_keys_nobody_keeps_reach_nothing():
+    """NaN in a K cluster that no Q cluster keeps: nothing else changes, but for the constant that dQ subtracts."""
+    svg2 = require_gpu()
+    N = 600
+    g = gen(11)
+    Q, K, V, dO = (randn(g, 1, 1, N, 64) for _ in range(4))
+    pl = plan(6, 1, 1, N, 6, 12, 0.6, unkept_k=(4,))
+    ref = sparse_step(svg2, pl, Q, K, V, dO, 0.125, perms=False)
+    lo, hi = pl["k_off"][0, 0, 4].item(), pl["k_off"][0, 0, 5].item()
+    assert hi > lo
+    K[:, :, lo:hi] = torch.nan
+    V[:, :, lo:hi] = torch.inf
+    got = sparse_step(svg2, pl, Q, K, V, dO, 0.125, perms=False)
+    for n in ("O", "lse"):
+        assert torch.equal(got[n], ref[n]), n
+    exact, tol = formulas(Q[0, 0], torch.where(K.isfinite(), K, 0.0)[0, 0], torch.where(V.isfinite(), V, 0.0)[0, 0],
+                          dO[0, 0], 0.125, rows_kept(pl, 0, 0, N), mean_key(K[0, 0]))
+    check(got["dQ"][0, 0], exact["dQ"], tol["dQ"], "dQ")
+    inside = torch.zeros(N, dtype=torch.bool, device="cuda")
+    inside[lo:hi] = True
+    for n in ("dK", "dV"):
+        assert torch.equal(got[n][0, 0, ~inside], ref[n][0, 0, ~inside]), n
+
+
+@pytest.mark.gpu
+def test_rows_outside_every_cluster_are_left_alone():
+    svg2 = require_gpu()
+    N = 500
+    g = gen(12)
+    Q, K, V, dO = (randn(g, 1, 1, N, 128) for _ in range(4))
+    pl = plan(7, 1, 1, N, 4, 4, 0.7)
+    pl["q_off"][0, 0, 4] = pl["k_off"][0, 0, 4] = N - 70  # the last clusters end early
+    pl["q_off"][0, 0, :4].clamp_(max=N - 70)
+    pl["k_off"][0, 0, :4].clamp_(max=N - 70)
+    got = sparse_step(svg2, pl, Q, K, V, dO, 0.1, perms=False)
+    for n in ("dQ", "dK", "dV"):
+        assert torch.isnan(got[n][0, 0, N - 70:]).all() and not torch.isnan(got[n][0, 0, :N - 70]).any(), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["twice", "past", "negative", "count"])
+def test_bad_plans_are_reported_and_write_nothing(what):
+    svg2 = require_gpu()
+    g = gen(13)
+    Q, K, V, dO = (randn(g, 1, 2, 400, 64) for _ in range(4))
+    pl = plan(8, 1, 2, 400, 5, 7, 0.8)
+    O, lse = torch.empty_like(Q), torch.empty(1, 2, 400, device="cuda")
+    args = [pl[n] for n in ("q_off", "k_off", "sel_count", "sel_idx")]
+    ws = svg2.sparse_bwd_workspace(1, 2, 400, 64, 5, 7)
+    svg2.svg2_sparse_attn_lse(Q, K, V, *args, 0.1, O, lse, ws)
+    row = int(pl["sel_count"][0, 1].argmax())
+    assert pl["sel_count"][0, 1, row] >= 2
+    if what == "twice":
+        pl["sel_idx"][0, 1, row, 1] = pl["sel_idx"][0, 1, row, 0]
+    elif what == "count":
+        pl["sel_count"][0, 1, row] = 8
+    else:
+        pl["sel_idx"][0, 1, row, 0] = 7 if what == "past" else -1
+    grads = [torch.full_like(Q, 3.0) for _ in range(3)]
+    svg2.svg2_sparse_attn_bwd(Q, K, V, O, lse, dO, *args, 0.1, *grads, ws)
+    with pytest.raises(svg2.Svg2Error) as e:
+        svg2.raise_on_device_error(ws)
+    assert e.value.code == 6
+    assert all((x == 3.0).all() for x in grads)
+    svg2.raise_on_device_error(ws)  # reading cleared it
+
+
+@pytest.mark.gpu
+def test_other_stream_and_captured_graph():
+    """The same bits on a side stream and from a replayed CUDA graph (after new inputs were copied in)."""
+    svg2 = require_gpu()
+    g = gen(14)
+    sets = [[randn(g, 1, 2, 700, 128) for _ in range(4)] for _ in range(2)]
+    pl = plan(9, 1, 2, 700, 6, 20, 0.6)
+    want = [(dense_step(svg2, *s, 0.09), sparse_step(svg2, pl, *s, 0.09)) for s in sets]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = dense_step(svg2, *sets[0], 0.09), sparse_step(svg2, pl, *sets[0], 0.09)
+    torch.cuda.synchronize()
+    assert same(got[0], want[0][0]) and same(got[1], want[0][1])
+    Q, K, V, dO = (x.clone() for x in sets[0])
+    O, dQ, dK, dV = (torch.empty_like(Q) for _ in range(4))
+    lse = torch.empty(1, 2, 700, device="cuda")
+    ws_d, ws_s = svg2.dense_bwd_workspace(1, 2, 700, 128), svg2.sparse_bwd_workspace(1, 2, 700, 128, 6, 20)
+    out2 = [torch.empty_like(Q) for _ in range(4)]
+    lse2 = torch.empty_like(lse)
+    args = [pl[n] for n in ("q_off", "k_off", "sel_count", "sel_idx")]
+
+    def step():
+        svg2.svg2_dense_attn_lse(Q, K, V, 0.09, O, lse, ws_d)
+        svg2.svg2_dense_attn_bwd(Q, K, V, O, lse, dO, 0.09, dQ, dK, dV, ws_d)
+        svg2.svg2_sparse_attn_lse(Q, K, V, *args, 0.09, out2[0], lse2, ws_s, perm_q=pl["perm_q"])
+        svg2.svg2_sparse_attn_bwd(Q, K, V, out2[0], lse2, dO, *args, 0.09, *out2[1:], ws_s, perm_q=pl["perm_q"],
+                                  perm_k=pl["perm_k"])
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in (1, 0):
+        for t, s in zip((Q, K, V, dO), sets[i]):
+            t.copy_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same({"O": O, "lse": lse, "dQ": dQ, "dK": dK, "dV": dV}, want[i][0])
+        assert same({"O": out2[0], "lse": lse2, "dQ": out2[1], "dK": out2[2], "dV": out2[3]}, want[i][1])
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once_on_their_own_workspaces():
+    svg2 = require_gpu()
+    g = gen(15)
+    sets = [[randn(g, 1, 4, 1500, 64) for _ in range(4)] for _ in range(2)]
+    want = [dense_step(svg2, *s, 0.1) for s in sets]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got, ws = [], []
+    for s, st in zip(sets, streams):
+        with torch.cuda.stream(st):
+            O, dQ, dK, dV = (torch.empty_like(s[0]) for _ in range(4))
+            lse = torch.empty(1, 4, 1500, device="cuda")
+            ws.append(svg2.dense_bwd_workspace(1, 4, 1500, 64))
+            for _ in range(5):
+                svg2.svg2_dense_attn_lse(*s[:3], 0.1, O, lse, ws[-1])
+                svg2.svg2_dense_attn_bwd(*s[:3], O, lse, s[3], 0.1, dQ, dK, dV, ws[-1])
+            got.append({"O": O, "lse": lse, "dQ": dQ, "dK": dK, "dV": dV})
+    torch.cuda.synchronize()
+    assert all(same(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.gpu
+def test_gradients_against_differences():
+    """Entries of dQ, dK, dV against central differences of the 64-bit loss sum(O o dO)."""
+    svg2 = require_gpu()
+    g = gen(16)
+    Q, K, V, dO = (randn(g, 1, 1, 40, 64) for _ in range(4))
+    got = dense_step(svg2, Q, K, V, dO, 0.125)
+    ref, tol = formulas(Q[0, 0], K[0, 0], V[0, 0], dO[0, 0], 0.125)
+    x = [t[0, 0].double() for t in (Q, K, V)]
+    h = 1e-5
+    for a, n in enumerate(("dQ", "dK", "dV")):
+        for i in range(0, 40 * 64, 331):
+            at = divmod(i, 64)
+            v = []
+            for sgn in (h, -h):
+                y = [t.clone() for t in x]
+                y[a][at] += sgn
+                v.append(((torch.softmax(y[0] @ y[1].T * 0.125, 1) @ y[2]) * dO[0, 0].double()).sum().item())
+            # differences: 1e-14 / h of rounding, h^2 times a third derivative of order 1
+            assert abs((v[0] - v[1]) / (2 * h) - got[n][0, 0][at].item()) <= tol[n][at].item() + 1e-8
+
+
+@pytest.mark.gpu
+def test_wait_that_runs_out_is_reported_and_leaves_the_workspace_usable():
+    svg2 = require_gpu()
+    g = gen(17)
+    Q, K, V, dO = (randn(g, 1, 2, 1000, 128) for _ in range(4))
+    want = dense_step(svg2, Q, K, V, dO, 0.1)
+    ws = svg2.dense_bwd_workspace(1, 2, 1000, 128)
+    O, dQ, dK, dV = (torch.empty_like(Q) for _ in range(4))
+    svg2.svg2_set_wait_budget(ws, 1)
+    svg2.svg2_dense_attn_bwd(Q, K, V, want["O"], want["lse"], dO, 0.1, dQ, dK, dV, ws)
+    code = svg2.svg2_check_status(ws)[0]
+    assert code == 5
+    svg2.svg2_set_wait_budget(ws, 0)
+    assert same(dense_step(svg2, Q, K, V, dO, 0.1, ws), want)
+
+
+def _chain64(layer, Q, K, V, dO, params, keep):
+    """The whole training layer in float64 with autograd: norm, attention over the kept pairs, loss sum(O o dO)."""
+    leaves = {n: t.detach().double().requires_grad_() for n, t in dict(Q=Q, K=K, V=V, **params).items()}
+
+    def norm(x, ga, be):
+        c = x - x.mean(-1, keepdim=True)
+        return c * ((c * c).mean(-1, keepdim=True) + layer.norm_eps) ** -0.5 * ga + be
+    q = norm(leaves["Q"], leaves["gamma_q"], leaves["beta_q"])
+    k = norm(leaves["K"], leaves["gamma_k"], leaves["beta_k"])
+    s = q @ k.mT * layer.scale
+    if keep is not None:
+        s = s.masked_fill(~keep, -torch.inf)
+    O = torch.softmax(s, -1) @ leaves["V"]
+    (O * dO.double()).sum().backward()
+    return O.detach(), {("d" + n): t.grad for n, t in leaves.items()}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sparse", [False, True])
+def test_training_layer(sparse):
+    """Norm, attention and both gradients as one layer, against the chain in 64 bits.  Seven roundings to bf16 lie on
+    the way (Qn, Kn, P, O, dS, the attention's gradient, dX), each at most U of its value; a change of U in q
+    and k moves a score by at most 2 U scale |q||k| ~ 2 U sqrt(d) for normed rows, and P by that factor: the
+    relative 2-norm stays below (7 + 2 sqrt(d)) U.  The parameters' gradients are sums over rows whose terms cancel
+    (dbeta_k is zero: adding one vector to all keys moves no probability), so the sums of the terms' magnitudes
+    take their place there: |dY| for beta, at most sqrt(d) |dY| for gamma (a normed row's entries)."""
+    svg2 = require_gpu()
+    B, H, N, d = 1, 2, 900, 64
+    g = gen(18)
+    Q, K, V, dO = (randn(g, B, H, N, d) for _ in range(4))
+    r = lambda c: c + 0.1 * torch.randn(d, device="cuda", generator=g)  # noqa: E731
+    params = dict(gamma_q=r(1), beta_q=r(0), gamma_k=r(1), beta_k=r(0))
+    prm = svg2.LayerParams(6, 12, 2, svg2.SVG2_INIT_KMEANSPP, 0.6, d ** -0.5, 1) if sparse else None
+    layer = svg2.TrainingLayer(B, H, N, d, prm, norm_eps=1e-5)
+    u = dict(uq=torch.rand(B, H, 6, dtype=torch.float64, device="cuda", generator=g),
+             uk=torch.rand(B, H, 12, dtype=torch.float64, device="cuda", generator=g)) if sparse else {}
+    with pytest.raises(ValueError):
+        layer.backward(dO)
+    O = layer.forward(Q, K, V, **params, **u)
+    grads = layer.backward(dO)
+    svg2.raise_on_device_error(layer.ws)
+    keep = None
+    if sparse:
+        m = layer.plan["mask"].bool()
+        lq, lk = layer.plan["labels_q"].long(), layer.plan["labels_k"].long()
+        keep = torch.stack([m[0, h][lq[0, h]][:, lk[0, h]] for h in range(H)])[None]
+        assert 0 < keep.float().mean() < 1
+    ref_O, ref = _chain64(layer, Q, K, V, dO, params, keep)
+    bound = (7 + 2 * d ** 0.5) * U
+    for n, x in dict(grads, O=O).items():
+        y = ref_O if n == "O" else ref[n]
+        size = torch.linalg.norm(y)
+        if n.startswith(("dbeta", "dgamma")):
+            terms = (layer.dQ if n.endswith("q") else layer.dK).double().abs().sum((0, 1, 2))
+            size = torch.linalg.norm(terms) * (d ** 0.5 if n.startswith("dgamma") else 1.0)
+        rel = (torch.linalg.norm(x.double() - y) / size).item()
+        assert rel <= bound, (n, rel)
+    if sparse:  # a second step from the cached centroids
+        layer.forward(Q, K, V, **params, init=svg2.SVG2_INIT_GIVEN)
+        layer.backward(dO)
+        svg2.raise_on_device_error(layer.ws)

@@ -214,3 +214,82 @@ def test_driver_layer_and_selftest(rec):
     assert rec.calls[-1][1][2] == 64
     with pytest.raises(ValueError):
         svg2.svg2_selftest_mma(A, _t(64, 127, dtype=bf16), V, _t(256, dtype=u8))
+
+
+@pytest.fixture
+def rec_training(rec, monkeypatch):
+    monkeypatch.setattr(svg2, "_device", lambda: -1)  # CPU tensors stand in for the current device's
+    monkeypatch.setattr(svg2, "_launch_stream", lambda stream, dev: None)
+    return rec
+
+
+def test_attention_training_calls(rec_training, monkeypatch):
+    rec = rec_training
+    B, H, N, d, nQ, nK = 1, 2, 300, 128, 4, 9
+    t = lambda: _t(B, H, N, d, dtype=bf16)  # noqa: E731
+    ws = _t(4096, dtype=u8)
+    fwd = dict(Q=t(), K=t(), V=t(), scale=0.1, O=t(), lse=_t(B, H, N, dtype=f32), ws=ws)
+    svg2.svg2_dense_attn_lse(**fwd)
+    name, a = rec.calls[-1]
+    assert name == "svg2_dense_attn_lse" and a[3:8] == (B, H, N, d, 0.1) and a[11] == 4096
+    _expect_refused(rec, svg2.svg2_dense_attn_lse, fwd, ["K", "V", "O", "lse"])
+    bwd = dict(fwd, dO=t(), dQ=t(), dK=t(), dV=t())
+    svg2.svg2_dense_attn_bwd(**bwd)
+    name, a = rec.calls[-1]
+    assert name == "svg2_dense_attn_bwd" and a[6:11] == (B, H, N, d, 0.1)
+    assert a[:6] == tuple(bwd[n].data_ptr() for n in ("Q", "K", "V", "O", "lse", "dO"))
+    assert a[11:15] == tuple(bwd[n].data_ptr() for n in ("dQ", "dK", "dV", "ws"))
+    _expect_refused(rec, svg2.svg2_dense_attn_bwd, bwd, ["K", "V", "O", "lse", "dO", "dQ", "dK", "dV"])
+    plan = dict(q_off=_t(B, H, nQ + 1, dtype=i32), k_off=_t(B, H, nK + 1, dtype=i32),
+                sel_count=_t(B, H, nQ, dtype=i32), sel_idx=_t(B, H, nQ, nK, dtype=i32))
+    sfwd = dict(Qp=t(), Kp=t(), Vp=t(), **plan, scale=0.1, O=t(), lse=_t(B, H, N, dtype=f32), ws=ws,
+                perm_q=_t(B, H, N, dtype=i32))
+    svg2.svg2_sparse_attn_lse(**sfwd)
+    name, a = rec.calls[-1]
+    assert name == "svg2_sparse_attn_lse" and a[7:14] == (B, H, N, d, nQ, nK, 0.1)
+    _expect_refused(rec, svg2.svg2_sparse_attn_lse, sfwd, ["Kp", "Vp", "sel_count", "sel_idx", "O", "lse", "perm_q"])
+    sbwd = dict(sfwd, dO=t(), dQ=t(), dK=t(), dV=t(), perm_k=_t(B, H, N, dtype=i32))
+    svg2.svg2_sparse_attn_bwd(**sbwd)
+    name, a = rec.calls[-1]
+    assert name == "svg2_sparse_attn_bwd" and a[10:17] == (B, H, N, d, nQ, nK, 0.1)
+    assert a[:10] == tuple(sbwd[n].data_ptr() for n in ("Qp", "Kp", "Vp", "O", "lse", "dO", "q_off", "k_off",
+                                                       "sel_count", "sel_idx"))
+    assert a[17:23] == tuple(sbwd[n].data_ptr() for n in ("perm_q", "perm_k", "dQ", "dK", "dV", "ws"))
+    _expect_refused(rec, svg2.svg2_sparse_attn_bwd, sbwd, ["Kp", "Vp", "O", "lse", "dO", "sel_count", "sel_idx", "dQ",
+                                                          "dK", "dV", "perm_q", "perm_k"])
+    for f, args in ((svg2.svg2_dense_attn_bwd, bwd), (svg2.svg2_sparse_attn_bwd, sbwd)):
+        n = len(rec.calls)
+        strided = _t(B, H, N, 2 * d, dtype=bf16)[..., :d]
+        with pytest.raises(ValueError):
+            f(**{**args, "dO": strided})              # a view with strides
+        with pytest.raises(ValueError):
+            f(**{**args, "lse": None})
+        with monkeypatch.context() as m:
+            m.setattr(svg2, "_device", lambda: 0)      # every tensor elsewhere than on the current device
+            with pytest.raises(ValueError, match="current device"):
+                f(**args)
+        assert len(rec.calls) == n
+
+
+def test_layer_norm_calls(rec_training):
+    rec = rec_training
+    X = _t(3, 5, 70, dtype=f32)
+    v, r = (lambda: _t(70, dtype=f32)), (lambda: _t(15, dtype=f32))
+    fwd = dict(X=X, gamma=v(), beta=v(), eps=1e-6, Y=_t(3, 5, 70, dtype=f32), mean=r(), rstd=r())
+    svg2.svg2_layer_norm(**fwd)
+    name, a = rec.calls[-1]
+    assert name == "svg2_layer_norm" and a[1] == svg2.SVG2_F32 and a[4:7] == (15, 70, 1e-6)
+    _expect_refused(rec, svg2.svg2_layer_norm, fwd, ["gamma", "beta", "Y", "mean", "rstd"])
+    svg2.svg2_layer_norm(X, None, None, 1e-6, X)
+    with pytest.raises(ValueError):
+        svg2.svg2_layer_norm(_t(3, 70, dtype=torch.float16), None, None, 1e-6, _t(3, 70, dtype=torch.float16))
+    bwd = dict(X=X, dY=_t(3, 5, 70, dtype=f32), gamma=v(), mean=r(), rstd=r(), dX=_t(3, 5, 70, dtype=f32), dgamma=v(),
+               dbeta=v(), ws=_t(4096, dtype=u8))
+    svg2.svg2_layer_norm_bwd(**bwd)
+    name, a = rec.calls[-1]
+    assert name == "svg2_layer_norm_bwd" and a[6:8] == (15, 70) and a[12] == 4096
+    _expect_refused(rec, svg2.svg2_layer_norm_bwd, bwd, ["dY", "gamma", "mean", "rstd", "dX", "dgamma", "dbeta"])
+    svg2.svg2_layer_norm_bwd(**{**bwd, "gamma": None, "dgamma": None, "dbeta": None})
+    for k in ("mean", "rstd", "ws"):
+        with pytest.raises(ValueError):
+            svg2.svg2_layer_norm_bwd(**{**bwd, k: None})
