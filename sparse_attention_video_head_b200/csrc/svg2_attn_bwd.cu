@@ -101,7 +101,7 @@ struct BwdArgs {
 };
 
 struct BwdBars {
-  uint64_t res_full, t1_full[2], t2_full[2], t1_empty[2], t2_empty[2], s_full[2], p_full, dp_full, ds_full, o_full,
+  uint64_t res_full, t1_full[2], t2_full[2], t1_empty[2], t2_empty[2], s_full[2], p_full[2], dp_full, ds_full[2], o_full,
       mma_done;
   uint32_t tmem_base;
   int32_t L, nranges;
@@ -359,13 +359,16 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
           mma_ss(d_tmem, sdesc_plain(smem_u32(seg_s), 128, 256), sdesc_plain(smem_u32(seg_s) + (1 + seg_stage) * kSegBytes, 128, 256),
                  id_s, 1u);
       };
-      // acc (+)= X T with X (P or dS, bf16) in TMEM, contraction over the tile's 128 rows
-      auto accumulate = [&](uint32_t acc, uint32_t x, uint32_t tb, bool add) {
+      // acc (+)= X T with X (P or dS, bf16) in TMEM, contraction over the tile's 128 rows, in the two chunks in
+      // which X is handed over: rows 0-31 and 64-95, then 32-63 and 96-127
+      auto accumulate = [&](uint32_t acc, uint32_t x, uint32_t tb, int chunk, bool add) {
         const uint64_t db = sdesc_sw128(tb, 16384, 1024);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
+        for (int u = 0; u < 4; ++u) {
+          const int ks = 2 * chunk + (u & 1) + (u >> 1) * 4;
           mma_ts(acc, x + (ks >> 2) * 64 + (ks & 3) * 8, db + static_cast<uint64_t>((ks * 16 * 128) >> 4), id_o,
-                 (add || ks > 0) ? 1u : 0u);
+                 (add || u > 0) ? 1u : 0u);
+        }
       };
       auto wait = [&](uint64_t* bar, int phase) {
         return mbar_wait(smem_u32(bar), phase & 1, st, kWhereAttnBwdMma, wb);
@@ -392,10 +395,14 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         const int sg = j & 1, ng = sg ^ 1;
         const bool more = j + 1 < T;
         if constexpr (KV) {
-          ok = wait(&bars->p_full, j);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (ok) ok = wait(&bars->p_full[c], j);
+            if (!ok) break;
+            tc_fence_after();
+            accumulate(tmem + Tm::acc1, tmem, t2 + sg * kTile, c, j > 0 || c > 0);  // dV += P^T dO
+          }
           if (!ok) break;
-          tc_fence_after();
-          accumulate(tmem + Tm::acc1, tmem, t2 + sg * kTile, j > 0);  // dV += P^T dO
           mma_commit(smem_u32(&bars->t2_empty[sg]));
         }
         if (more) {
@@ -407,11 +414,15 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
           product(tmem + (KV ? 0u : ng * Tm::s1), r1, t1 + ng * kTile, ng);
           mma_commit(smem_u32(&bars->s_full[KV ? 0 : ng]));
         }
-        ok = wait(&bars->ds_full, j);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (ok) ok = wait(&bars->ds_full[c], j);
+          if (!ok) break;
+          tc_fence_after();
+          accumulate(tmem + Tm::acc2, tmem + Tm::dp, t1 + sg * kTile, c, j > 0 || c > 0);  // dK += dS^T Q | dQ += dS K
+          if constexpr (SPLIT) accumulate(tmem + Tm::acc2, tmem + Tm::dp + 32, t1 + sg * kTile, c, true);
+        }
         if (!ok) break;
-        tc_fence_after();
-        accumulate(tmem + Tm::acc2, tmem + Tm::dp, t1 + sg * kTile, j > 0);  // dK += dS^T Q | dQ += dS K
-        if constexpr (SPLIT) accumulate(tmem + Tm::acc2, tmem + Tm::dp + 32, t1 + sg * kTile, true);
         mma_commit(smem_u32(&bars->t1_empty[sg]));
         if (more) {
           ok = wait_tile(&bars->t2_full[ng], (j + 1) >> 1);
@@ -582,59 +593,78 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, st, kWhereAttnBwdSoftmax, wb));
     };
     const bool exact_delta = SPLIT && T == 1 && (!KV || (DENSE && a.N <= 128));
+    auto all_softmax_warps = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    auto hand_over = [&](uint64_t* bar) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(bar));
+    };
     float2 r_sum = make_float2(0.f, 0.f);  // query unit: this half's sum of the row's rounded dS
     bool ok = true;
+    // Every tile goes in two chunks of 32 columns: the loads of the second run under the first's arithmetic, and
+    // the MMA warp starts on the first while the second is computed.
     for (int j = 0; j < T; ++j) {
       const int sg = j & 1;
       const float* st_l = stats + sg * 256 + half * 64;  // key unit: -lse log2(e) of this half's columns,
       const float* st_d = st_l + 128;                    // and -delta
       ok = KV ? wait(&bars->s_full[0], j) : wait(&bars->s_full[sg], j >> 1);
       if (ok && KV) ok = wait(&bars->t1_full[sg], j >> 1);  // the copies of lse and delta (already complete)
-      if (!ok) break;
-      tc_fence_after();
       const uint32_t t_s = tmem + lane_off + (KV ? 0u : sg * Tm::s1) + half * 64;
       const uint32_t t_dp = tmem + lane_off + Tm::dp + half * 64;
       uint32_t sv[64];
-      tmem_ld32p(t_s, sv);
-      tmem_ld32p(t_s + 32, sv + 32);
-      tmem_wait_ld();
-      const int valid = L - j * 128 - half * 64;
-      if (valid < 64) {  // past the stream's end: P = 0
-#pragma unroll
-        for (int e = 0; e < 64; ++e)
-          if (e >= valid) sv[e] = __float_as_uint(-INFINITY);
-      }
-      // P = 2^(s log2(e) - lse log2(e))
       float2 p[32];
+      if (ok) {
+        tc_fence_after();
+        tmem_ld32p(t_s, sv);
+        tmem_wait_ld();
+        tmem_ld32p(t_s + 32, sv + 32);
+        const int valid = L - j * 128 - half * 64;
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float4 l4;
-        if constexpr (KV) l4 = *reinterpret_cast<const float4*>(st_l + 2 * e);
-        else l4 = make_float4(nl_row, nl_row, nl_row, nl_row);
+        for (int c = 0; c < 2; ++c) {
+          if (c == 1) tmem_wait_ld();
+          if (valid < 64) {  // past the stream's end: P = 0
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float2 t = fma2(make_float2(__uint_as_float(sv[2 * (e + u)]), __uint_as_float(sv[2 * (e + u) + 1])), scl,
-                                u == 0 ? make_float2(l4.x, l4.y) : make_float2(l4.z, l4.w));
-          p[e + u] = (((e + u) & 15) >= 16 - kBwdCubicPairs) ? exp2_cubic2(t)
-                                                             : make_float2(fast_exp2(t.x), fast_exp2(t.y));
+            for (int e = 32 * c; e < 32 * c + 32; ++e)
+              if (e >= valid) sv[e] = __float_as_uint(-INFINITY);
+          }
+          // P = 2^(s log2(e) - lse log2(e))
+#pragma unroll
+          for (int e = 16 * c; e < 16 * c + 16; e += 2) {
+            float4 l4;
+            if constexpr (KV) l4 = *reinterpret_cast<const float4*>(st_l + 2 * e);
+            else l4 = make_float4(nl_row, nl_row, nl_row, nl_row);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float2 t = fma2(make_float2(__uint_as_float(sv[2 * (e + u)]), __uint_as_float(sv[2 * (e + u) + 1])),
+                                    scl, u == 0 ? make_float2(l4.x, l4.y) : make_float2(l4.z, l4.w));
+              p[e + u] = (((e + u) & 15) >= 16 - kBwdCubicPairs) ? exp2_cubic2(t)
+                                                                 : make_float2(fast_exp2(t.x), fast_exp2(t.y));
+            }
+          }
+          if constexpr (KV) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(p[16 * c + e].x, p[16 * c + e].y);
+            tmem_st16(t_s + 16 * c, pk);
+            if (c == 0) hand_over(&bars->p_full[0]);
+          }
         }
+        ok = wait(&bars->dp_full, j);  // (does not depend on this tile's P)
       }
-      if constexpr (KV) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(p[e].x, p[e].y);
-        tmem_st32(t_s, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full));
+      if (!ok) {
+        if (exact_delta) {  // (the warps that got further meet here)
+          all_softmax_warps();
+          if constexpr (KV) all_softmax_warps();
+        }
+        break;
       }
-      ok = wait(&bars->dp_full, j);
-      if (!ok) break;
       tc_fence_after();
       tmem_ld32p(t_dp, sv);
-      tmem_ld32p(t_dp + 32, sv + 32);
+      if constexpr (KV) hand_over(&bars->p_full[1]);
       tmem_wait_ld();
+      tmem_ld32p(t_dp + 32, sv + 32);
+      if constexpr (SPLIT) tmem_wait_ld();  // (the second halves of dS go where dP's second chunk is)
       if (exact_delta) {
         // delta_i = sum_j P_ij dP_ij in float32
         if constexpr (KV) {  // over the lanes and the four warps: this CTA holds every key of the plane
@@ -658,64 +688,57 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
           float* red = scratch + (warp & 3) * 128 + half * 64 + 2 * lane;  // lane l ends with columns 2l, 2l + 1
           red[0] = x[0];
           red[1] = x[1];
-          asm volatile("bar.sync 1, 256;" ::: "memory");
+          all_softmax_warps();
           if (half == 0) {
             const float* c = scratch + row;
             stats[128 + row] = -((c[0] + c[128]) + (c[256] + c[384]));
           }
-          asm volatile("bar.sync 1, 256;" ::: "memory");
+          all_softmax_warps();
         } else {  // over the row's two halves
           float2 x = make_float2(0.f, 0.f);
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             x = fma2(p[e], make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), x);
           stats[256 + half * 128 + row] = x.x + x.y;
-          asm volatile("bar.sync 1, 256;" ::: "memory");
+          all_softmax_warps();
           nd_row = -(stats[256 + row] + stats[384 + row]);
         }
       }
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {  // 32 columns at a time
-        uint32_t hi[16];
-        auto ds_pair = [&](int e) {
-          float2 d2;
-          if constexpr (KV) d2 = *reinterpret_cast<const float2*>(st_d + 32 * c + 2 * e);
-          else d2 = make_float2(nd_row, nd_row);
-          return mul2(p[16 * c + e], add2(make_float2(__uint_as_float(sv[32 * c + 2 * e]),
-                                                      __uint_as_float(sv[32 * c + 2 * e + 1])), d2));
-        };
+      for (int c = 0; c < 2; ++c) {
+        if (c == 1) tmem_wait_ld();
+        uint32_t hi[16], lo[SPLIT ? 16 : 1];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 ds = ds_pair(e);
-          hi[e] = pack_bf16x2(ds.x, ds.y);
+        for (int e = 0; e < 16; e += 2) {
+          float4 d4;
+          if constexpr (KV) d4 = *reinterpret_cast<const float4*>(st_d + 32 * c + 2 * e);
+          else d4 = make_float4(nd_row, nd_row, nd_row, nd_row);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int k = 16 * c + e + u;
+            const float2 ds = mul2(p[k], add2(make_float2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])),
+                                              u == 0 ? make_float2(d4.x, d4.y) : make_float2(d4.z, d4.w)));
+            hi[e + u] = pack_bf16x2(ds.x, ds.y);
+            if constexpr (SPLIT)
+              lo[e + u] = pack_bf16x2(ds.x - bf16lo_to_f32(hi[e + u]), ds.y - bf16hi_to_f32(hi[e + u]));
+          }
         }
         tmem_st16(t_dp + 16 * c, hi);
+        if constexpr (SPLIT) tmem_st16(t_dp + 32 + 16 * c, lo);
+        hand_over(&bars->ds_full[c]);
         if constexpr (!KV) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r_sum = add2(r_sum, make_float2(bf16lo_to_f32(hi[e]), bf16hi_to_f32(hi[e])));
-        }
-        if constexpr (SPLIT) {
-#pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float2 ds = ds_pair(e);
-            hi[e] = pack_bf16x2(ds.x - bf16lo_to_f32(hi[e]), ds.y - bf16hi_to_f32(hi[e]));
-          }
-          tmem_st16(t_dp + 32 + 16 * c, hi);
-          if constexpr (!KV) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) r_sum = add2(r_sum, make_float2(bf16lo_to_f32(hi[e]), bf16hi_to_f32(hi[e])));
+            r_sum = add2(r_sum, make_float2(bf16lo_to_f32(hi[e]), bf16hi_to_f32(hi[e])));
+            if constexpr (SPLIT) r_sum = add2(r_sum, make_float2(bf16lo_to_f32(lo[e]), bf16hi_to_f32(lo[e])));
           }
         }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->ds_full));
     }
     float r_row = 0.f;
     if constexpr (!KV) {  // both halves' sums (the streamed lse buffer is free in a query unit)
       stats[half * 128 + row] = r_sum.x + r_sum.y;
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      all_softmax_warps();
       r_row = stats[row] + stats[128 + row];
     }
     if (ok && T > 0) ok = wait(&bars->o_full, 0);
@@ -864,10 +887,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(smem_u32(&bars->t1_empty[i]), 1);
       mbar_init(smem_u32(&bars->t2_empty[i]), 1);
       mbar_init(smem_u32(&bars->s_full[i]), 1);
+      mbar_init(smem_u32(&bars->p_full[i]), 8);
+      mbar_init(smem_u32(&bars->ds_full[i]), 8);
     }
-    mbar_init(smem_u32(&bars->p_full), 8);
     mbar_init(smem_u32(&bars->dp_full), 1);
-    mbar_init(smem_u32(&bars->ds_full), 8);
     mbar_init(smem_u32(&bars->o_full), 1);
     mbar_init(smem_u32(&bars->mma_done), 1);
     fence_mbar_init();
