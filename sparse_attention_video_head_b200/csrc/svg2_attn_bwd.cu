@@ -16,7 +16,7 @@
 // edges cost no padding; rows past the stream's end are zeros.
 //   warps 0-7   P and dS: TMEM lanes = resident rows, warps 0-3 the tile's columns 0-63, 4-7 64-127
 //   warp 8      TMEM allocator and MMA issuer
-//   warps 9-11  (9 alone when dense) range table, then the tiles' producers, and the streamed queries' lse, delta
+//   warps 9-11  (9 alone when dense) range table, then the tiles' producers
 // P and dS are rounded to bf16 for the products (as P is in the forward); both stay float32 until then.
 // A row of dS sums to zero, so dQ does not depend on what all keys have in common; the rounded dS, with delta
 // from a bf16 O, sums to some r_i instead, and dQ would carry scale r_i times that common part, which
@@ -51,27 +51,44 @@ constexpr int kBwdCubicPairs = 8;
 
 template <int D>
 constexpr uint32_t bwd_tile_bytes() { return 128u * D * 2u; }
+// One more step of the S and dP products, 16 deep, adds what depends on the streamed row alone (key unit) or masks pairs
+// (MULTI units), so that the warps that compute P and dS read nothing but TMEM: their loads from shared memory
+// wait behind the products' operand reads.  The resident side A holds ones in columns 0-2 and in column 4 + c for
+// the rows of the unit's cluster c; the streamed side B holds
+//   S, columns 0-2   -lse / scale as three bf16 (24 bits), so that S' = S - lse / scale      (key unit)
+//   S, column 4 + c  the penalty -3.4e38 where cluster c does not keep the streamed row        (MULTI)
+//   dP, columns 0-2  -delta as three bf16, so that dP' = dP - delta                             (key unit)
+// and zeros elsewhere.  Both [128, 16], K-major without swizzle: the first 8 columns of all rows, 16 bytes each, then
+// the other 8.
+constexpr uint32_t kStepBytes = 4096, kStepPlane = 2048;
+constexpr int kBwdMaxSegments = 12;
+constexpr uint32_t kSegPenalty = 0xff7fu;  // bf16 -3.39e38
+
 template <int D>
 constexpr uint32_t bwd_smem() {
-  return 6 * bwd_tile_bytes<D>() + 1024 /*align*/ + 4 * 512 /*lse, delta of two stages*/ + 4096 /*range starts*/ +
-         4096 + 64 /*range offsets*/ + 2048 /*range segments*/ + 3 * 4096 /*segment operands*/ + 256 /*barriers*/;
+  return 6 * bwd_tile_bytes<D>() + 1024 /*align*/ + 2048 /*row sums*/ + 4096 /*range starts*/ +
+         4096 + 64 /*range offsets*/ + 2048 /*range segments*/ + 5 * kStepBytes /*A, B of S and dP by stage*/ +
+         256 /*barriers*/;
 }
-// MULTI units: pairs that a row's own cluster does not keep get S = -3.4e38 from one more step of the S product,
-// 16 deep: A holds a one in the column of the row's cluster, B that column's penalty (0 or the lowest bf16) for the
-// streamed row.  A select per score instead made the key unit's softmax its longest part (8 x 12480 with 256
-// K clusters, every pair kept: 2.69 ms against 2.04).  Both operands [128, 16] are K-major without swizzle: 8 x 16-byte
-// blocks, the two of a row 128 bytes apart, 8-row groups 256 bytes apart.
-constexpr uint32_t kSegBytes = 4096;
-constexpr uint32_t kSegPenalty = 0xff7fu;  // bf16 -3.39e38
-__device__ __forceinline__ uint32_t seg_offset(int row) { return (row >> 3) * 256 + (row & 7) * 16; }
-// two bf16 per word, 16 values: the penalty where the bit of `keep` is clear
-__device__ __forceinline__ void store_seg(uint8_t* dst, uint32_t keep) {
-  uint32_t w[8];
+static_assert(bwd_smem<128>() <= 227 * 1024, "shared memory");
+
+// Column 4 + c of a row's S operand: the penalty where bit c of `keep` is clear.
+__device__ __forceinline__ void store_seg(uint8_t* b, int row, uint32_t keep) {
+  uint32_t w[6];
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
+  for (int k = 0; k < 6; ++k)
     w[k] = ((keep >> (2 * k)) & 1u ? 0u : kSegPenalty) | ((keep >> (2 * k + 1)) & 1u ? 0u : kSegPenalty << 16);
-  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4*>(dst + 128) = make_uint4(w[4], w[5], w[6], w[7]);
+  *reinterpret_cast<uint2*>(b + row * 16 + 8) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint4*>(b + kStepPlane + row * 16) = make_uint4(w[2], w[3], w[4], w[5]);
+}
+// v as the sum of three bf16 (the first alone when it is not finite), then five zeros
+__device__ __forceinline__ uint4 three_bf16(float v) {
+  const uint32_t hi = pack_bf16x2(v, 0.f) & 0xffffu;
+  const float r1 = v - __uint_as_float(hi << 16);
+  const uint32_t mid = pack_bf16x2(r1, 0.f) & 0xffffu;
+  const uint32_t lo = pack_bf16x2(r1 - __uint_as_float(mid << 16), 0.f) & 0xffffu;
+  const bool finite = fabsf(__uint_as_float(hi << 16)) < INFINITY;
+  return make_uint4(finite ? hi | (mid << 16) : hi, finite ? lo : 0u, 0u, 0u);
 }
 
 // Streams of up to this many tiles hand dS over as two bf16 numbers (its rounding, and the rest) and take one
@@ -91,6 +108,7 @@ struct BwdArgs {
   const BwdUnit *k_units, *q_units;                    // [BH, per_head]
   const int32_t *perm_q, *perm_k;
   const float *neg_lse2, *neg_delta;                   // [BH, N] -lse log2(e), -delta, by permuted row
+  const uint4 *lse_step, *delta_step;                  // [BH, N] three_bf16 of -lse / scale, of -delta
   const float* k_mean;                                 // [BH, D]
   const __nv_bfloat16 *Q, *K, *V, *dO;                 // the tensors of the maps
   __nv_bfloat16 *dQ, *dK, *dV;
@@ -107,10 +125,6 @@ struct BwdBars {
   int32_t L, nranges;
 };
 
-// 4-byte asynchronous copy; bytes = 0 writes a zero and reads nothing.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 
 // ------------------------------------------------------------------------------------------------
 // delta_i = dO_i . O_i and the scaled log-sum-exp, by permuted row; with perm, dO's rows in permuted
@@ -154,8 +168,10 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
                                                        const float* __restrict__ lse, const int32_t* __restrict__ perm,
                                                        const uint4* __restrict__ K, int N, long long rows,
                                                        int BH, float* __restrict__ neg_lse2,
-                                                       float* __restrict__ neg_delta, uint4* __restrict__ dOp,
-                                                       float* __restrict__ k_mean, DeviceStatus* st) {
+                                                       float* __restrict__ neg_delta, uint4* __restrict__ lse_step,
+                                                       uint4* __restrict__ delta_step, float inv_scale,
+                                                       uint4* __restrict__ dOp, float* __restrict__ k_mean,
+                                                       DeviceStatus* st) {
   if (static_cast<int>(blockIdx.x) < BH) {
     mean_key<D>(K, blockIdx.x, N, k_mean);
     return;
@@ -197,6 +213,8 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
         const float l = lse[r];
         neg_lse2[r] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row without keys has P = 0
         neg_delta[r] = -acc;
+        lse_step[r] = three_bf16(l == -INFINITY ? 0.f : -l * inv_scale);  // (such a row is in no stream)
+        delta_step[r] = three_bf16(-acc);
       }
     }
   }
@@ -213,8 +231,6 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
 // clusters' streams, never longer than the two, and the pairs that a row's own cluster does not keep are masked.
 // On 8 heads of 12480 tokens in 64 / 256 clusters (49 rows per K cluster) at 60 % kept, ... .
 // ------------------------------------------------------------------------------------------------
-constexpr int kBwdMaxSegments = 16;
-
 // Packs clusters [c0, c1) into units; `emit` takes them in order.  Returns their number.
 template <class Emit>
 __device__ __forceinline__ int pack_units(const int32_t* off, int c0, int c1, int N, Emit&& emit) {
@@ -331,7 +347,7 @@ struct BwdTmem {
 template <int D, bool DENSE, bool KV, bool SPLIT, bool MULTI>
 __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, const BwdUnit un, const int bh,
                                          uint8_t* smem, BwdBars* bars, float* stats, const int32_t* r_start,
-                                         const int32_t* r_cum, const uint16_t* r_seg, uint8_t* seg_s, float* scratch, const long long wb) {
+                                         const int32_t* r_cum, const uint16_t* r_seg, uint8_t* step_s, float* scratch, const long long wb) {
   constexpr uint32_t kTile = bwd_tile_bytes<D>();
   constexpr int kHalves = D / 64;   // 128-byte swizzle atoms across a row
   constexpr int kSteps = D / 16;    // instructions of one S or dP product
@@ -347,18 +363,20 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
     if (elect_one() && T > 0) {
       const uint32_t id_s = idesc_bf16_f32(128, 128, 0);  // both operands K-major
       const uint32_t id_o = idesc_bf16_f32(128, D, 1);    // B = a streamed tile read row-major (MN-major)
-      // D[slot] = R x T^T, contraction over d
-      auto product = [&](uint32_t d_tmem, uint32_t ra, uint32_t tb, int seg_stage) {
+      // D[slot] = R x T^T, contraction over d, and the step's columns (B at `step`, 0: none)
+      const uint32_t step_a = smem_u32(step_s), step_b = step_a + kStepBytes;  // B of S, dP of stage 0, then of stage 1
+      auto product = [&](uint32_t d_tmem, uint32_t ra, uint32_t tb, uint32_t step) {
         const uint64_t da = sdesc_sw128(ra, 16, 1024), db = sdesc_sw128(tb, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < kSteps; ++ks) {
           const uint64_t off = static_cast<uint64_t>(((ks >> 2) * 16384 + (ks & 3) * 32) >> 4);
           mma_ss(d_tmem, da + off, db + off, id_s, ks > 0 ? 1u : 0u);
         }
-        if (MULTI && seg_stage >= 0)
-          mma_ss(d_tmem, sdesc_plain(smem_u32(seg_s), 128, 256), sdesc_plain(smem_u32(seg_s) + (1 + seg_stage) * kSegBytes, 128, 256),
-                 id_s, 1u);
+        if (step != 0u)
+          mma_ss(d_tmem, sdesc_plain(step_a, kStepPlane, 128), sdesc_plain(step, kStepPlane, 128), id_s, 1u);
       };
+      auto s_step = [&](int stage) { return KV || MULTI ? step_b + stage * 2 * kStepBytes : 0u; };
+      auto dp_step = [&](int stage) { return KV ? step_b + (stage * 2 + 1) * kStepBytes : 0u; };
       // acc (+)= X T with X (P or dS, bf16) in TMEM, contraction over the tile's 128 rows, in the two chunks in
       // which X is handed over: rows 0-31 and 64-95, then 32-63 and 96-127
       auto accumulate = [&](uint32_t acc, uint32_t x, uint32_t tb, int chunk, bool add) {
@@ -375,19 +393,19 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       };
       auto wait_tile = [&](uint64_t* bar, int phase) {
         const bool landed = wait(bar, phase);
-        if (!DENSE) fence_proxy_async_smem();  // rows gathered by cp.async (generic proxy)
+        if (!DENSE) fence_proxy_async_smem();  // rows gathered by cp.async, segments stored (generic proxy)
         return landed;
       };
       bool ok = wait(&bars->res_full, 0) && wait_tile(&bars->t1_full[0], 0);
       if (ok) {
         tc_fence_after();
-        product(tmem, r1, t1, 0);
+        product(tmem, r1, t1, s_step(0));
         mma_commit(smem_u32(&bars->s_full[0]));
         ok = wait_tile(&bars->t2_full[0], 0);
       }
       if (ok) {
         tc_fence_after();
-        product(tmem + Tm::dp, r2, t2, -1);
+        product(tmem + Tm::dp, r2, t2, dp_step(0));
         mma_commit(smem_u32(&bars->dp_full));
         if (!KV) mma_commit(smem_u32(&bars->t2_empty[0]));
       }
@@ -411,7 +429,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
           ok = wait_tile(&bars->t1_full[ng], (j + 1) >> 1);
           if (!ok) break;
           tc_fence_after();
-          product(tmem + (KV ? 0u : ng * Tm::s1), r1, t1 + ng * kTile, ng);
+          product(tmem + (KV ? 0u : ng * Tm::s1), r1, t1 + ng * kTile, s_step(ng));
           mma_commit(smem_u32(&bars->s_full[KV ? 0 : ng]));
         }
 #pragma unroll
@@ -428,7 +446,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
           ok = wait_tile(&bars->t2_full[ng], (j + 1) >> 1);
           if (!ok) break;
           tc_fence_after();
-          product(tmem + Tm::dp, r2, t2 + ng * kTile, -1);
+          product(tmem + Tm::dp, r2, t2 + ng * kTile, dp_step(ng));
           mma_commit(smem_u32(&bars->dp_full));
           if (!KV) mma_commit(smem_u32(&bars->t2_empty[ng]));
         }
@@ -456,42 +474,38 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         tma_load_3d(r2 + h * 16384, &maps.m[KV ? 2 : 3], h * 64, un.row0, bh, bar);
       }
     }
-    auto tma_tile = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int row) {
-      mbar_arrive_expect_tx(bar, kTile);
+    auto tma_tile = [&](const CUtensorMap* m, uint32_t dst, uint32_t bar, int row, uint32_t more_bytes) {
+      mbar_arrive_expect_tx(bar, kTile + more_bytes);
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * 16384, m, h * 64, row, bh, bar);
     };
     const size_t plane = static_cast<size_t>(bh) * a.N;
-    const float* nl = a.neg_lse2 + plane;
-    const float* nd = a.neg_delta + plane;
+    const uint32_t step_b = smem_u32(step_s) + kStepBytes;  // B of S, dP of stage 0, then of stage 1
     int n1 = 0, n2 = 0;  // tiles requested of each streamed operand
     bool ok = true;
     auto wait_empty = [&](uint64_t* bar, int j) {
       return j < 2 || __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(bar), ((j >> 1) - 1) & 1, st,
                                                               kWhereAttnBwdProducer, 32, wb));
     };
-    // -lse log2(e) and -delta of plane row `row` into column c of the stage (row < 0: zeros)
-    auto stat = [&](int sg, int c, int row) {
-      const uint32_t dst = smem_u32(stats + sg * 256 + c);
-      cp_async4(dst, nl + max(row, 0), row >= 0 ? 4u : 0u);
-      cp_async4(dst + 512, nd + max(row, 0), row >= 0 ? 4u : 0u);
-    };
     if constexpr (DENSE) {
       for (int j = 0; j < T; ++j) {
         const int sg = j & 1;
-        const uint32_t b1 = smem_u32(&bars->t1_full[sg]);
+        const uint32_t b1 = smem_u32(&bars->t1_full[sg]), b2 = smem_u32(&bars->t2_full[sg]);
+        // the rows' step operands: as many as the plane still has (columns past it are masked)
+        const uint32_t bytes = KV ? min(128, a.N - j * 128) * 16u : 0u;
         ok = wait_empty(&bars->t1_empty[sg], j);
         if (!ok) break;
-        if (leader) tma_tile(m1, t1 + sg * kTile, b1, j * 128);
-        if constexpr (KV) {
-#pragma unroll
-          for (int c = lane; c < 128; c += 32) stat(sg, c, j * 128 + c < a.N ? j * 128 + c : -1);
-          cp_async_mbar_arrive(b1);
+        if (leader) {
+          tma_tile(m1, t1 + sg * kTile, b1, j * 128, bytes);
+          if (KV) bulk_load(step_b + sg * 2 * kStepBytes, a.lse_step + plane + j * 128, bytes, b1);
         }
         n1 = j + 1;
         ok = wait_empty(&bars->t2_empty[sg], j);
         if (!ok) break;
-        if (leader) tma_tile(m2, t2 + sg * kTile, smem_u32(&bars->t2_full[sg]), j * 128);
+        if (leader) {
+          tma_tile(m2, t2 + sg * kTile, b2, j * 128, bytes);
+          if (KV) bulk_load(step_b + (sg * 2 + 1) * kStepBytes, a.delta_step + plane + j * 128, bytes, b2);
+        }
         n2 = j + 1;
       }
     } else {
@@ -531,19 +545,25 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         ok = wait_empty(&bars->t1_empty[sg], j);
         if (!ok) break;
         if (whole) {
-          if (leader) tma_tile(m1, t1 + sg * kTile, b1, first);
+          if (leader) tma_tile(m1, t1 + sg * kTile, b1, first, 0u);
         } else {
           if (leader) mbar_arrive(b1);
           gather(t1 + sg * kTile, s1);
         }
+        // a stream row's step operand: of the query (key unit), then its segments (MULTI; 8 bytes hold the three bf16)
+        auto row_step = [&](uint32_t dst, const uint4* src, int c, int g) {
+          const uint4* from = src + plane + max(g, 0);
+          if (MULTI) cp_async8_zfill(dst + c * 16, from, g >= 0);
+          else cp_async16_zfill(dst + c * 16, from, g >= 0);
+        };
         if constexpr (KV) {
-          stat(sg, wr0 + lane, g0);
-          if (32 + lane < nrw) stat(sg, wr0 + 32 + lane, g1);
+          row_step(step_b + sg * 2 * kStepBytes, a.lse_step, wr0 + lane, g0);
+          if (32 + lane < nrw) row_step(step_b + sg * 2 * kStepBytes, a.lse_step, wr0 + 32 + lane, g1);
         }
         cp_async_mbar_arrive(b1);
         if constexpr (MULTI) {  // (plain stores: an arrival of their own orders them)
           auto segs = [&](int c, int g, int e) {
-            if (g >= 0) store_seg(seg_s + (1 + sg) * kSegBytes + seg_offset(c), r_seg[e]);
+            if (g >= 0) store_seg(step_s + (1 + sg * 2) * kStepBytes, c, r_seg[e]);
           };
           segs(wr0 + lane, g0, e0);
           if (32 + lane < nrw) segs(wr0 + 32 + lane, g1, e1);
@@ -554,10 +574,14 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         ok = wait_empty(&bars->t2_empty[sg], j);
         if (!ok) break;
         if (whole) {
-          if (leader) tma_tile(m2, t2 + sg * kTile, b2, first);
+          if (leader) tma_tile(m2, t2 + sg * kTile, b2, first, 0u);
         } else {
           if (leader) mbar_arrive(b2);
           gather(t2 + sg * kTile, s2);
+        }
+        if constexpr (KV) {
+          row_step(step_b + (sg * 2 + 1) * kStepBytes, a.delta_step, wr0 + lane, g0);
+          if (32 + lane < nrw) row_step(step_b + (sg * 2 + 1) * kStepBytes, a.delta_step, wr0 + 32 + lane, g1);
         }
         cp_async_mbar_arrive(b2);
         n2 = j + 1;
@@ -606,10 +630,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
     // the MMA warp starts on the first while the second is computed.
     for (int j = 0; j < T; ++j) {
       const int sg = j & 1;
-      const float* st_l = stats + sg * 256 + half * 64;  // key unit: -lse log2(e) of this half's columns,
-      const float* st_d = st_l + 128;                    // and -delta
       ok = KV ? wait(&bars->s_full[0], j) : wait(&bars->s_full[sg], j >> 1);
-      if (ok && KV) ok = wait(&bars->t1_full[sg], j >> 1);  // the copies of lse and delta (already complete)
       const uint32_t t_s = tmem + lane_off + (KV ? 0u : sg * Tm::s1) + half * 64;
       const uint32_t t_dp = tmem + lane_off + Tm::dp + half * 64;
       uint32_t sv[64];
@@ -628,26 +649,19 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
             for (int e = 32 * c; e < 32 * c + 32; ++e)
               if (e >= valid) sv[e] = __float_as_uint(-INFINITY);
           }
-          // P = 2^(s log2(e) - lse log2(e))
+          // P = 2^(s log2(e) - lse log2(e)); in a key unit S' holds the lse already
 #pragma unroll
-          for (int e = 16 * c; e < 16 * c + 16; e += 2) {
-            float4 l4;
-            if constexpr (KV) l4 = *reinterpret_cast<const float4*>(st_l + 2 * e);
-            else l4 = make_float4(nl_row, nl_row, nl_row, nl_row);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float2 t = fma2(make_float2(__uint_as_float(sv[2 * (e + u)]), __uint_as_float(sv[2 * (e + u) + 1])),
-                                    scl, u == 0 ? make_float2(l4.x, l4.y) : make_float2(l4.z, l4.w));
-              p[e + u] = (((e + u) & 15) >= 16 - kBwdCubicPairs) ? exp2_cubic2(t)
-                                                                 : make_float2(fast_exp2(t.x), fast_exp2(t.y));
-            }
+          for (int e = 16 * c; e < 16 * c + 16; ++e) {
+            const float2 x = make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1]));
+            const float2 t = KV ? mul2(x, scl) : fma2(x, scl, make_float2(nl_row, nl_row));
+            p[e] = ((e & 15) >= 16 - kBwdCubicPairs) ? exp2_cubic2(t) : make_float2(fast_exp2(t.x), fast_exp2(t.y));
           }
           if constexpr (KV) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(p[16 * c + e].x, p[16 * c + e].y);
             tmem_st16(t_s + 16 * c, pk);
-            if (c == 0) hand_over(&bars->p_full[0]);
+            hand_over(&bars->p_full[c]);
           }
         }
         ok = wait(&bars->dp_full, j);  // (does not depend on this tile's P)
@@ -661,19 +675,19 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       }
       tc_fence_after();
       tmem_ld32p(t_dp, sv);
-      if constexpr (KV) hand_over(&bars->p_full[1]);
       tmem_wait_ld();
       tmem_ld32p(t_dp + 32, sv + 32);
       if constexpr (SPLIT) tmem_wait_ld();  // (the second halves of dS go where dP's second chunk is)
       if (exact_delta) {
-        // delta_i = sum_j P_ij dP_ij in float32
+        // delta_i = sum_j P_ij dP_ij in float32 (key unit: what is missing in dP' = dP - delta)
         if constexpr (KV) {  // over the lanes and the four warps: this CTA holds every key of the plane
           float x[32];
+          const bool key = row < un.nrows;  // (the rows past it have a dP' too)
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             const float2 lo = p[i >> 1], hi = p[16 + (i >> 1)];
-            const float a0 = ((i & 1) ? lo.y : lo.x) * __uint_as_float(sv[i]);
-            const float a1 = ((i & 1) ? hi.y : hi.x) * __uint_as_float(sv[32 + i]);
+            const float a0 = key ? ((i & 1) ? lo.y : lo.x) * __uint_as_float(sv[i]) : 0.f;
+            const float a1 = key ? ((i & 1) ? hi.y : hi.x) * __uint_as_float(sv[32 + i]) : 0.f;
             const bool up = (lane & 16) != 0;
             x[i] = (up ? a1 : a0) + __shfl_xor_sync(0xffffffffu, up ? a0 : a1, 16);
           }
@@ -709,19 +723,15 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         if (c == 1) tmem_wait_ld();
         uint32_t hi[16], lo[SPLIT ? 16 : 1];
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          float4 d4;
-          if constexpr (KV) d4 = *reinterpret_cast<const float4*>(st_d + 32 * c + 2 * e);
-          else d4 = make_float4(nd_row, nd_row, nd_row, nd_row);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int k = 16 * c + e + u;
-            const float2 ds = mul2(p[k], add2(make_float2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])),
-                                              u == 0 ? make_float2(d4.x, d4.y) : make_float2(d4.z, d4.w)));
-            hi[e + u] = pack_bf16x2(ds.x, ds.y);
-            if constexpr (SPLIT)
-              lo[e + u] = pack_bf16x2(ds.x - bf16lo_to_f32(hi[e + u]), ds.y - bf16hi_to_f32(hi[e + u]));
-          }
+        for (int e = 0; e < 16; ++e) {
+          const int k = 16 * c + e;
+          float2 x = make_float2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
+          if constexpr (!KV) x = add2(x, make_float2(nd_row, nd_row));
+          else if constexpr (SPLIT)
+            if (exact_delta) x = add2(x, *reinterpret_cast<const float2*>(stats + 128 + half * 64 + 2 * k));
+          const float2 ds = mul2(p[k], x);
+          hi[e] = pack_bf16x2(ds.x, ds.y);
+          if constexpr (SPLIT) lo[e] = pack_bf16x2(ds.x - bf16lo_to_f32(hi[e]), ds.y - bf16hi_to_f32(hi[e]));
         }
         tmem_st16(t_dp + 16 * c, hi);
         if constexpr (SPLIT) tmem_st16(t_dp + 32 + 16 * c, lo);
@@ -736,7 +746,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       }
     }
     float r_row = 0.f;
-    if constexpr (!KV) {  // both halves' sums (the streamed lse buffer is free in a query unit)
+    if constexpr (!KV) {  // both halves' sums of the row
       stats[half * 128 + row] = r_sum.x + r_sum.y;
       all_softmax_warps();
       r_row = stats[row] + stats[128 + row];
@@ -870,19 +880,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   constexpr uint32_t kTile = bwd_tile_bytes<D>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* stats = reinterpret_cast<float*>(smem + 6 * kTile);  // [stage][lse | delta][128]
+  float* stats = reinterpret_cast<float*>(smem + 6 * kTile);  // sums over rows' halves, or columns
   int32_t* r_start = reinterpret_cast<int32_t*>(stats + 512);
   int32_t* r_cum = r_start + kBwdMaxRanges;  // kBwdMaxRanges + 1 entries
   uint16_t* r_seg = reinterpret_cast<uint16_t*>(r_cum + kBwdMaxRanges + 16);
-  uint8_t* seg_s = reinterpret_cast<uint8_t*>(r_seg + kBwdMaxRanges);  // this unit's rows, then two streamed tiles'
-  BwdBars* bars = reinterpret_cast<BwdBars*>(seg_s + 3 * kSegBytes);
+  uint8_t* step_s = reinterpret_cast<uint8_t*>(r_seg + kBwdMaxRanges);  // A, then B of S and of dP for both stages
+  BwdBars* bars = reinterpret_cast<BwdBars*>(step_s + 5 * kStepBytes);
   const int warp = threadIdx.x >> 5;
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->res_full), 1);
     for (int i = 0; i < 2; ++i) {
-      // the TMA bytes (or the leader's arrival), each producer lane's own copies and, when sparse, its plain stores
-      mbar_init(smem_u32(&bars->t1_full[i]), dense ? (kv ? 33 : 1) : 193);
+      // the TMA bytes (or the leader's arrival); when sparse, each producer lane's own copies and plain stores
+      mbar_init(smem_u32(&bars->t1_full[i]), dense ? 1 : 193);
       mbar_init(smem_u32(&bars->t2_full[i]), dense ? 1 : 97);
       mbar_init(smem_u32(&bars->t1_empty[i]), 1);
       mbar_init(smem_u32(&bars->t2_empty[i]), 1);
@@ -899,16 +909,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
   }
-  if (!dense && warp < 4) {  // this row's cluster among the unit's
-    const int row = threadIdx.x;
-    const int32_t* off = kv ? a.k_off + static_cast<size_t>(bh) * (a.nK + 1) : a.q_off + static_cast<size_t>(bh) * (a.nQ + 1);
-    int seg = 0;
-    while (seg + 1 < un.nseg && off[un.cluster + seg + 1] <= un.row0 + row) ++seg;
-    uint32_t w[8];
+  if (kv || !dense) {  // the step operands: A, and zeros in B
+    if (warp < 4) {
+      const int row = threadIdx.x;
+      int seg = 0;  // this row's cluster among the unit's
+      if constexpr (!dense) {
+        const int32_t* off = kv ? a.k_off + static_cast<size_t>(bh) * (a.nK + 1) : a.q_off + static_cast<size_t>(bh) * (a.nQ + 1);
+        while (seg + 1 < un.nseg && off[un.cluster + seg + 1] <= un.row0 + row) ++seg;
+      }
+      uint32_t w[8] = {0x3f803f80u, 0x3f80u};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = seg == 2 * k ? 0x3f80u : (seg == 2 * k + 1 ? 0x3f800000u : 0u);
-    *reinterpret_cast<uint4*>(seg_s + seg_offset(row)) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4*>(seg_s + seg_offset(row) + 128) = make_uint4(w[4], w[5], w[6], w[7]);
+      for (int k = 0; k < 6; ++k) w[2 + k] = seg == 2 * k ? 0x3f80u : (seg == 2 * k + 1 ? 0x3f800000u : 0u);
+      *reinterpret_cast<uint4*>(step_s + row * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(step_s + kStepPlane + row * 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else if (warp < 8) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<uint4*>(step_s + kStepBytes + (k * 128 + threadIdx.x - 128) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
     fence_proxy_async_smem();
   }
   if (warp == kBwdProducerWarp) {
@@ -922,7 +940,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   else asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBwdSoftmaxRegs) : "memory");
   float* scratch = reinterpret_cast<float*>(r_start);
 #define SVG2_BWD_UNIT(KV, SPLIT, MULTI) \
-  bwd_unit<D, dense, KV, SPLIT, MULTI>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, r_seg, seg_s, scratch, wb)
+  bwd_unit<D, dense, KV, SPLIT, MULTI>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, r_seg, step_s, scratch, wb)
   if constexpr (dense) {
     constexpr bool kShort = KIND == BwdKind::kDenseShort;
     if (kv) SVG2_BWD_UNIT(true, kShort, false);
@@ -959,6 +977,7 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   bwd_prep_kernel<D><<<grid + BH, 256, 0, s>>>(static_cast<const uint4*>(in.O), static_cast<const uint4*>(in.dO),
                                                in.lse, in.perm_q, static_cast<const uint4*>(in.K), N, rows,
                                                BH, sc.neg_lse2, sc.neg_delta,
+                                               sc.lse_step, sc.delta_step, 1.f / scale,
                                                in.perm_q != nullptr ? static_cast<uint4*>(sc.dOp) : nullptr,
                                                sc.k_mean, st);
   cudaError_t e = cudaGetLastError();
@@ -990,6 +1009,8 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   a.neg_lse2 = sc.neg_lse2;
   a.neg_delta = sc.neg_delta;
   a.k_mean = sc.k_mean;
+  a.lse_step = sc.lse_step;
+  a.delta_step = sc.delta_step;
   a.dQ = static_cast<__nv_bfloat16*>(in.dQ);
   a.dK = static_cast<__nv_bfloat16*>(in.dK);
   a.dV = static_cast<__nv_bfloat16*>(in.dV);

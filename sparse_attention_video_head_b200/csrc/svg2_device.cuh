@@ -97,6 +97,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same question without the wait that try_wait may include.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Bounded wait on the phase with the given parity.  Gives up (returns false) once `budget` clock
 // cycles have passed since the first unsuccessful poll (checked after every poll), or as soon as
 // the status word, read every 64 polls, shows an error raised anywhere in the grid.
@@ -441,6 +454,10 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 // The same copy, or 16 zero bytes (src is not read) when `in` is false.
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16u : 0u) : "memory");
+}
+// Eight bytes of it (both addresses 8-byte aligned).
+__device__ __forceinline__ void cp_async8_zfill(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(in ? 8u : 0u) : "memory");
 }
 // Arrive on `bar` once every cp.async this thread has issued so far has landed (the barrier's
 // expected count includes this arrival: .noinc).

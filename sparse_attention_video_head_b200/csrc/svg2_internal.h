@@ -202,6 +202,7 @@ inline int bwd_max_units_per_head(int N, int n) { return N / 128 + n; }
 
 struct BwdScratch {
   float *neg_lse2, *neg_delta;  // [BH, N] -lse log2(e) and -dO.O by permuted row
+  uint4 *lse_step, *delta_step;  // [BH, N] -lse / scale and -delta as three bf16 each
   float* k_mean;                // [BH, d] mean of (a sample of) the plane's K rows
   void* dOp;                    // [BH, N, d] dO in permuted order (used when perm_q is given)
   uint32_t* keepers;            // [BH, nK, ceil(nQ / 32)] bit i: Q cluster i keeps the K cluster
@@ -214,6 +215,8 @@ inline void carve_bwd(Carve& c, int BH, int N, int d, int nQ, int nK, BwdScratch
   const size_t rows = static_cast<size_t>(BH) * N;
   s.neg_lse2 = c.take<float>(rows);
   s.neg_delta = c.take<float>(rows);
+  s.lse_step = c.take<uint4>(rows);
+  s.delta_step = c.take<uint4>(rows);
   s.k_mean = c.take<float>(static_cast<size_t>(BH) * d);
   s.dOp = nQ > 0 ? c.take<uint16_t>(rows * d) : nullptr;
   s.keepers = nQ > 0 ? c.take<uint32_t>(static_cast<size_t>(BH) * nK * ((nQ + 31) / 32)) : nullptr;
