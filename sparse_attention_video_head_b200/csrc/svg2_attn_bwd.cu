@@ -227,86 +227,89 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
 //
 // A unit costs as many tiles as its stream is long, however few of its 128 rows are used, and clusters
 // rarely end on a multiple of 128.  So what is left of a cluster after its full tiles shares a unit with the
-// rows that follow whenever that saves the next cluster a unit: the joint stream is the union of the
-// clusters' streams, never longer than the two, and the pairs that a row's own cluster does not keep are masked.
-// On 8 heads of 12480 tokens in 64 / 256 clusters (49 rows per K cluster) at 60 % kept, ... .
+// rows that follow; the joint stream is the union of the clusters' streams, and the pairs that a row's own
+// cluster does not keep are masked.  On 8 heads of 12480 tokens in 64 / 256 clusters (49 rows per K cluster),
+// 60 % kept, units of one cluster each took 2.91 ms, shared ones MEASURE.
 // ------------------------------------------------------------------------------------------------
-// Packs clusters [c0, c1) into units; `emit` takes them in order.  Returns their number.
+
+// One warp packs clusters [c0, c1) into units, lane w holding word w of the clusters' bits; lane 0 calls
+// emit(i, unit) in order.  Returns their number.
+//
+// A unit takes t rows of the next cluster if that leaves the cluster a unit less (a union is never longer than
+// its parts), or if the stream grows by less than half of what t of a unit's 128 rows cost: the room serves
+// the rows to come.  (Half: over the plans of the tests and the 720p layer the sum of the streams came out
+// within 3 % of the best of 0, 0.5, 0.7, 1 and always, each of which loses 5 to 35 % on some.)
 template <class Emit>
-__device__ __forceinline__ int pack_units(const int32_t* off, int c0, int c1, int N, Emit&& emit) {
+__device__ __forceinline__ int pack_units(const int32_t* off, const uint32_t* bits, int W, int c0, int c1, int N,
+                                          Emit&& emit) {
+  const int lane = threadIdx.x & 31;
   int count = 0;
   int first = 0, row0 = 0, rows = 0, last = 0;  // the unit that can still take rows (rows = 0: none)
+  uint32_t joint = 0u;                          // what any of its clusters keeps or is kept by
   int end = off[c0];
   for (int j = c0; j < c1; ++j) {
+    const uint32_t mine = lane < W ? bits[j * W + lane] : 0u;
     int start = end;
     end = off[j + 1];
     int left = end - start;
     if (start < 0 || left <= 0 || start > N - left) continue;  // empty, or malformed offsets
-    if (rows > 0 && row0 + rows == start && j - first < kBwdMaxSegments) {
+    if (rows > 0 && rows < 128 && row0 + rows == start && j - first < kBwdMaxSegments) {
       const int t = min(128 - rows, left);
-      if (((left - t + 127) >> 7) < ((left + 127) >> 7)) {
+      const int added = __reduce_add_sync(0xffffffffu, __popc(mine & ~joint));
+      const int all = __reduce_add_sync(0xffffffffu, __popc(mine | joint));
+      if (((left - t + 127) >> 7) < ((left + 127) >> 7) || added * 256 < t * all) {
         rows += t;
         last = j;
+        joint |= mine;
         start += t;
         left -= t;
       }
     }
     if (left > 0) {
-      if (rows > 0) emit(count++, BwdUnit{first, row0, rows, last - first + 1});
-      for (; left >= 128; start += 128, left -= 128) emit(count++, BwdUnit{j, start, 128, 1});
+      if (rows > 0) {
+        if (lane == 0) emit(count, BwdUnit{first, row0, rows, last - first + 1});
+        ++count;
+      }
+      for (; left >= 128; start += 128, left -= 128) {
+        if (lane == 0) emit(count, BwdUnit{j, start, 128, 1});
+        ++count;
+      }
       first = last = j;
       row0 = start;
       rows = left;
+      joint = mine;
     }
   }
-  if (rows > 0) emit(count++, BwdUnit{first, row0, rows, last - first + 1});
+  if (rows > 0) {
+    if (lane == 0) emit(count, BwdUnit{first, row0, rows, last - first + 1});
+    ++count;
+  }
   return count;
 }
 
-// One warp packs a plane's clusters: each lane its own run of at least 16 (units do not cross runs, which
-// costs at most 31 units of a plane and keeps the scan short: a single thread took 70 us for 500 clusters).
-__device__ void write_units(const int32_t* off, int n, int N, int per_head, BwdUnit* out, DeviceStatus* st) {
-  const int lane = threadIdx.x & 31;
-  const int run = max(16, (n + 31) / 32);
-  const int c0 = min(n, lane * run), c1 = min(n, c0 + run);
-  for (int j = c0; j < c1; ++j) SVG2_DEBUG_CHECK(off[j] >= 0 && off[j + 1] >= off[j] && off[j + 1] <= N, st, kWherePlan, j, off[j]);
-  const int mine = pack_units(off, c0, c1, N, [](int, const BwdUnit&) {});
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  const int base = incl - mine;
-  pack_units(off, c0, c1, N, [&](int i, const BwdUnit& u) {
-    if (base + i < per_head) out[base + i] = u;
-  });
-  for (int s = __shfl_sync(0xffffffffu, incl, 31) + lane; s < per_head; s += 32) out[s] = BwdUnit{0, 0, 0, 0};
-}
+constexpr int kPlanRun = 32;  // clusters that one warp packs; units do not cross runs (at most 31 units of a plane)
+constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
+constexpr size_t kPlanSmem = 200 * 1024;  // the selection's bits both ways, if they fit
 
-__global__ void __launch_bounds__(512) bwd_plan_kernel(const int32_t* __restrict__ q_off,
-                                                       const int32_t* __restrict__ k_off,
-                                                       const int32_t* __restrict__ sel_count,
-                                                       const int32_t* __restrict__ sel_idx, int N, int nQ, int nK,
-                                                       uint32_t* __restrict__ keepers, uint32_t* __restrict__ kept,
-                                                       BwdUnit* __restrict__ k_units, int k_per_head,
-                                                       BwdUnit* __restrict__ q_units, int q_per_head,
-                                                       DeviceStatus* st) {
-  extern __shared__ uint32_t bits[];  // [nK, WQ], then [14 warps][WK]
+__global__ void __launch_bounds__(kPlanThreads)
+    bwd_plan_kernel(const int32_t* __restrict__ q_off, const int32_t* __restrict__ k_off,
+                    const int32_t* __restrict__ sel_count, const int32_t* __restrict__ sel_idx, int N, int nQ, int nK,
+                    uint32_t* keepers, uint32_t* kept, bool kept_in_smem, BwdUnit* __restrict__ k_units,
+                    int k_per_head, BwdUnit* __restrict__ q_units, int q_per_head, DeviceStatus* st) {
+  extern __shared__ uint32_t k_bits[];  // [nK, WQ], then [nQ, WK] if it fits, else [16 warps][WK]
   __shared__ int32_t k_offsets[kMaxClustersAssign + 1], q_offsets[kMaxClustersAssign + 1];
+  __shared__ int32_t base[2 * (kMaxClustersAssign / kPlanRun) + 2];  // units before each run, K's runs then Q's
   const int WQ = (nQ + 31) / 32, WK = (nK + 31) / 32;
-  const int bh = blockIdx.x;
-  for (int w = threadIdx.x; w < nK * WQ; w += blockDim.x) bits[w] = 0u;
-  for (int i = threadIdx.x; i <= nK; i += blockDim.x) k_offsets[i] = k_off[static_cast<size_t>(bh) * (nK + 1) + i];
-  for (int i = threadIdx.x; i <= nQ; i += blockDim.x) q_offsets[i] = q_off[static_cast<size_t>(bh) * (nQ + 1) + i];
+  const int bh = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int w = threadIdx.x; w < nK * WQ; w += kPlanThreads) k_bits[w] = 0u;
+  for (int i = threadIdx.x; i <= nK; i += kPlanThreads) k_offsets[i] = k_off[static_cast<size_t>(bh) * (nK + 1) + i];
+  for (int i = threadIdx.x; i <= nQ; i += kPlanThreads) q_offsets[i] = q_off[static_cast<size_t>(bh) * (nQ + 1) + i];
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t* mine = bits + nK * WQ + warp * WK;
-  // warps 14 and 15 write the units while the others turn the selection into bits
-  if (warp == 14) write_units(k_offsets, nK, N, k_per_head, k_units + static_cast<size_t>(bh) * k_per_head, st);
-  if (warp == 15) write_units(q_offsets, nQ, N, q_per_head, q_units + static_cast<size_t>(bh) * q_per_head, st);
-  for (int i = warp; i < nQ && warp < 14; i += 14) {
+  uint32_t* kept_g = kept + static_cast<size_t>(bh) * nQ * WK;
+  uint32_t* q_bits_s = k_bits + nK * WQ;
+  for (int i = warp; i < nQ; i += kPlanWarps) {
     const size_t row = static_cast<size_t>(bh) * nQ + i;
+    uint32_t* mine = q_bits_s + (kept_in_smem ? i : warp) * WK;
     for (int w = lane; w < WK; w += 32) mine[w] = 0u;
     __syncwarp();
     int cnt = sel_count[row];
@@ -317,17 +320,50 @@ __global__ void __launch_bounds__(512) bwd_plan_kernel(const int32_t* __restrict
     for (int e = lane; e < cnt; e += 32) {
       const int j = sel_idx[row * nK + e];
       const uint32_t bit = 1u << (i & 31);
-      if (j < 0 || j >= nK || (atomicOr(&bits[j * WQ + (i >> 5)], bit) & bit) != 0u)
+      if (j < 0 || j >= nK || (atomicOr(&k_bits[j * WQ + (i >> 5)], bit) & bit) != 0u)
         raise_status(st, kStatusDeviceBounds, kWherePlan, i, j);
       else
         atomicOr(&mine[j >> 5], 1u << (j & 31));
     }
     __syncwarp();
-    for (int w = lane; w < WK; w += 32) kept[row * WK + w] = mine[w];
+    for (int w = lane; w < WK; w += 32) kept_g[i * WK + w] = mine[w];
     __syncwarp();
   }
   __syncthreads();
-  for (int w = threadIdx.x; w < nK * WQ; w += blockDim.x) keepers[static_cast<size_t>(bh) * nK * WQ + w] = bits[w];
+  for (int w = threadIdx.x; w < nK * WQ; w += kPlanThreads) keepers[static_cast<size_t>(bh) * nK * WQ + w] = k_bits[w];
+  // units: each run is packed twice, to count its units and to write them
+  const int runs_k = (nK + kPlanRun - 1) / kPlanRun, runs_q = (nQ + kPlanRun - 1) / kPlanRun;
+  const uint32_t* q_bits = kept_in_smem ? q_bits_s : kept_g;
+  auto pack = [&](int r, auto&& emit) {
+    const bool k = r < runs_k;
+    const int c0 = (k ? r : r - runs_k) * kPlanRun;
+    return pack_units(k ? k_offsets : q_offsets, k ? k_bits : q_bits, k ? WQ : WK, c0, min(k ? nK : nQ, c0 + kPlanRun),
+                      N, emit);
+  };
+  for (int r = warp; r < runs_k + runs_q; r += kPlanWarps) {
+    const int n = pack(r, [](int, const BwdUnit&) {});
+    if (lane == 0) base[r + 1 + (r >= runs_k ? 1 : 0)] = n;
+  }
+  for (int i = threadIdx.x; i < nK; i += kPlanThreads) SVG2_DEBUG_CHECK(k_offsets[i] >= 0 && k_offsets[i + 1] >= k_offsets[i] && k_offsets[i + 1] <= N, st, kWherePlan, i, k_offsets[i]);
+  for (int i = threadIdx.x; i < nQ; i += kPlanThreads) SVG2_DEBUG_CHECK(q_offsets[i] >= 0 && q_offsets[i + 1] >= q_offsets[i] && q_offsets[i + 1] <= N, st, kWherePlan, i, q_offsets[i]);
+  __syncthreads();
+  if (threadIdx.x < 2) {  // base: [0, K's runs ..., total], [0, Q's runs ..., total]
+    int32_t* b = base + (threadIdx.x == 0 ? 0 : runs_k + 1);
+    b[0] = 0;
+    for (int r = 0; r < (threadIdx.x == 0 ? runs_k : runs_q); ++r) b[r + 1] += b[r];
+  }
+  __syncthreads();
+  BwdUnit* ku = k_units + static_cast<size_t>(bh) * k_per_head;
+  BwdUnit* qu = q_units + static_cast<size_t>(bh) * q_per_head;
+  for (int r = warp; r < runs_k + runs_q; r += kPlanWarps) {
+    const bool k = r < runs_k;
+    const int b = base[r + (k ? 0 : 1)];
+    pack(r, [&](int i, const BwdUnit& u) {
+      if (b + i < (k ? k_per_head : q_per_head)) (k ? ku : qu)[b + i] = u;
+    });
+  }
+  for (int i = base[runs_k] + threadIdx.x; i < k_per_head; i += kPlanThreads) ku[i] = BwdUnit{0, 0, 0, 0};
+  for (int i = base[runs_k + 1 + runs_q] + threadIdx.x; i < q_per_head; i += kPlanThreads) qu[i] = BwdUnit{0, 0, 0, 0};
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -485,7 +521,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
     bool ok = true;
     auto wait_empty = [&](uint64_t* bar, int j) {
       return j < 2 || __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(bar), ((j >> 1) - 1) & 1, st,
-                                                              kWhereAttnBwdProducer, 32, wb));
+                                                              kWhereAttnBwdProducer, 100, wb));
     };
     if constexpr (DENSE) {
       for (int j = 0; j < T; ++j) {
@@ -990,11 +1026,13 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   a.k_per_head = dense ? (N + 127) / 128 : bwd_max_units_per_head(N, nK);
   a.q_per_head = dense ? (N + 127) / 128 : bwd_max_units_per_head(N, nQ);
   if (!dense) {
-    const uint32_t bits = (static_cast<uint32_t>(nK) * ((nQ + 31) / 32) + 16u * ((nK + 31) / 32)) * 4;
-    e = cudaFuncSetAttribute(bwd_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 131072 + 2048);
+    const size_t k_bytes = static_cast<size_t>(nK) * ((nQ + 31) / 32) * 4, row = static_cast<size_t>((nK + 31) / 32) * 4;
+    const bool fits = k_bytes + nQ * row <= kPlanSmem;
+    e = cudaFuncSetAttribute(bwd_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPlanSmem));
     if (e != cudaSuccess) return e;
-    bwd_plan_kernel<<<BH, 512, bits, s>>>(in.q_off, in.k_off, in.sel_count, in.sel_idx, N, nQ, nK, sc.keepers,
-                                          sc.kept, sc.k_units, a.k_per_head, sc.q_units, a.q_per_head, st);
+    bwd_plan_kernel<<<BH, kPlanThreads, k_bytes + (fits ? nQ : kPlanWarps) * row, s>>>(
+        in.q_off, in.k_off, in.sel_count, in.sel_idx, N, nQ, nK, sc.keepers, sc.kept, fits, sc.k_units, a.k_per_head,
+        sc.q_units, a.q_per_head, st);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
