@@ -233,14 +233,14 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
 // ------------------------------------------------------------------------------------------------
 
 // One warp packs clusters [c0, c1) into units, lane w holding word w of the clusters' bits; lane 0 calls
-// emit(i, unit) in order.  Returns their number.
+// emit(i, unit) in order.
 //
 // A unit takes t rows of the next cluster if that leaves the cluster a unit less (a union is never longer than
 // its parts), or if the stream grows by less than half of what t of a unit's 128 rows cost: the room serves
 // the rows to come.  (Half: over the plans of the tests and the 720p layer the sum of the streams came out
 // within 3 % of the best of 0, 0.5, 0.7, 1 and always, each of which loses 5 to 35 % on some.)
 template <class Emit>
-__device__ __forceinline__ int pack_units(const int32_t* off, const uint32_t* bits, int W, int c0, int c1, int N,
+__device__ __forceinline__ void pack_units(const int32_t* off, const uint32_t* bits, int W, int c0, int c1, int N,
                                           Emit&& emit) {
   const int lane = threadIdx.x & 31;
   int count = 0;
@@ -282,13 +282,11 @@ __device__ __forceinline__ int pack_units(const int32_t* off, const uint32_t* bi
   }
   if (rows > 0) {
     if (lane == 0) emit(count, BwdUnit{first, row0, rows, last - first + 1});
-    ++count;
   }
-  return count;
 }
 
 constexpr int kPlanRun = 32;  // clusters that one warp packs; units do not cross runs (at most 31 units of a plane)
-constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr size_t kPlanSmem = 200 * 1024;  // the selection's bits both ways, if they fit
 
 __global__ void __launch_bounds__(kPlanThreads)
@@ -296,12 +294,15 @@ __global__ void __launch_bounds__(kPlanThreads)
                     const int32_t* __restrict__ sel_count, const int32_t* __restrict__ sel_idx, int N, int nQ, int nK,
                     uint32_t* keepers, uint32_t* kept, bool kept_in_smem, BwdUnit* __restrict__ k_units,
                     int k_per_head, BwdUnit* __restrict__ q_units, int q_per_head, DeviceStatus* st) {
-  extern __shared__ uint32_t k_bits[];  // [nK, WQ], then [nQ, WK] if it fits, else [16 warps][WK]
+  extern __shared__ uint32_t k_bits[];  // [nK, WQ], then [nQ, WK] if it fits, else [32 warps][WK]
   __shared__ int32_t k_offsets[kMaxClustersAssign + 1], q_offsets[kMaxClustersAssign + 1];
-  __shared__ int32_t base[2 * (kMaxClustersAssign / kPlanRun) + 2];  // units before each run, K's runs then Q's
   const int WQ = (nQ + 31) / 32, WK = (nK + 31) / 32;
   const int bh = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int w = threadIdx.x; w < nK * WQ; w += kPlanThreads) k_bits[w] = 0u;
+  BwdUnit* ku = k_units + static_cast<size_t>(bh) * k_per_head;
+  BwdUnit* qu = q_units + static_cast<size_t>(bh) * q_per_head;
+  for (int i = threadIdx.x; i < k_per_head; i += kPlanThreads) ku[i] = BwdUnit{0, 0, 0, 0};
+  for (int i = threadIdx.x; i < q_per_head; i += kPlanThreads) qu[i] = BwdUnit{0, 0, 0, 0};
   for (int i = threadIdx.x; i <= nK; i += kPlanThreads) k_offsets[i] = k_off[static_cast<size_t>(bh) * (nK + 1) + i];
   for (int i = threadIdx.x; i <= nQ; i += kPlanThreads) q_offsets[i] = q_off[static_cast<size_t>(bh) * (nQ + 1) + i];
   __syncthreads();
@@ -317,13 +318,19 @@ __global__ void __launch_bounds__(kPlanThreads)
       if (lane == 0) raise_status(st, kStatusDeviceBounds, kWherePlan, i, cnt);
       cnt = 0;
     }
-    for (int e = lane; e < cnt; e += 32) {
-      const int j = sel_idx[row * nK + e];
-      const uint32_t bit = 1u << (i & 31);
-      if (j < 0 || j >= nK || (atomicOr(&k_bits[j * WQ + (i >> 5)], bit) & bit) != 0u)
-        raise_status(st, kStatusDeviceBounds, kWherePlan, i, j);
-      else
-        atomicOr(&mine[j >> 5], 1u << (j & 31));
+    for (int e0 = lane; e0 < cnt; e0 += 256) {  // eight loads in flight
+      int j[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) j[u] = e0 + 32 * u < cnt ? __ldg(sel_idx + row * nK + e0 + 32 * u) : -1;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (e0 + 32 * u >= cnt) break;
+        const uint32_t bit = 1u << (i & 31);
+        if (j[u] < 0 || j[u] >= nK || (atomicOr(&k_bits[j[u] * WQ + (i >> 5)], bit) & bit) != 0u)
+          raise_status(st, kStatusDeviceBounds, kWherePlan, i, j[u]);
+        else
+          atomicOr(&mine[j[u] >> 5], 1u << (j[u] & 31));
+      }
     }
     __syncwarp();
     for (int w = lane; w < WK; w += 32) kept_g[i * WK + w] = mine[w];
@@ -331,39 +338,23 @@ __global__ void __launch_bounds__(kPlanThreads)
   }
   __syncthreads();
   for (int w = threadIdx.x; w < nK * WQ; w += kPlanThreads) keepers[static_cast<size_t>(bh) * nK * WQ + w] = k_bits[w];
-  // units: each run is packed twice, to count its units and to write them
+  // units: a run's go from the slot that the runs before it cannot reach (a run of n clusters and m rows has at
+  // most n + m / 128), the slots between stay empty
   const int runs_k = (nK + kPlanRun - 1) / kPlanRun, runs_q = (nQ + kPlanRun - 1) / kPlanRun;
   const uint32_t* q_bits = kept_in_smem ? q_bits_s : kept_g;
-  auto pack = [&](int r, auto&& emit) {
+  for (int r = warp; r < runs_k + runs_q; r += kPlanWarps) {
     const bool k = r < runs_k;
     const int c0 = (k ? r : r - runs_k) * kPlanRun;
-    return pack_units(k ? k_offsets : q_offsets, k ? k_bits : q_bits, k ? WQ : WK, c0, min(k ? nK : nQ, c0 + kPlanRun),
-                      N, emit);
-  };
-  for (int r = warp; r < runs_k + runs_q; r += kPlanWarps) {
-    const int n = pack(r, [](int, const BwdUnit&) {});
-    if (lane == 0) base[r + 1 + (r >= runs_k ? 1 : 0)] = n;
+    const int32_t* off = k ? k_offsets : q_offsets;
+    const int base = min(max(off[c0], 0), N) / 128 + c0, most = k ? k_per_head : q_per_head;
+    BwdUnit* out = k ? ku : qu;
+    pack_units(off, k ? k_bits : q_bits, k ? WQ : WK, c0, min(k ? nK : nQ, c0 + kPlanRun), N,
+               [&](int i, const BwdUnit& u) {
+                 if (base + i < most) out[base + i] = u;
+               });
   }
   for (int i = threadIdx.x; i < nK; i += kPlanThreads) SVG2_DEBUG_CHECK(k_offsets[i] >= 0 && k_offsets[i + 1] >= k_offsets[i] && k_offsets[i + 1] <= N, st, kWherePlan, i, k_offsets[i]);
   for (int i = threadIdx.x; i < nQ; i += kPlanThreads) SVG2_DEBUG_CHECK(q_offsets[i] >= 0 && q_offsets[i + 1] >= q_offsets[i] && q_offsets[i + 1] <= N, st, kWherePlan, i, q_offsets[i]);
-  __syncthreads();
-  if (threadIdx.x < 2) {  // base: [0, K's runs ..., total], [0, Q's runs ..., total]
-    int32_t* b = base + (threadIdx.x == 0 ? 0 : runs_k + 1);
-    b[0] = 0;
-    for (int r = 0; r < (threadIdx.x == 0 ? runs_k : runs_q); ++r) b[r + 1] += b[r];
-  }
-  __syncthreads();
-  BwdUnit* ku = k_units + static_cast<size_t>(bh) * k_per_head;
-  BwdUnit* qu = q_units + static_cast<size_t>(bh) * q_per_head;
-  for (int r = warp; r < runs_k + runs_q; r += kPlanWarps) {
-    const bool k = r < runs_k;
-    const int b = base[r + (k ? 0 : 1)];
-    pack(r, [&](int i, const BwdUnit& u) {
-      if (b + i < (k ? k_per_head : q_per_head)) (k ? ku : qu)[b + i] = u;
-    });
-  }
-  for (int i = base[runs_k] + threadIdx.x; i < k_per_head; i += kPlanThreads) ku[i] = BwdUnit{0, 0, 0, 0};
-  for (int i = base[runs_k + 1 + runs_q] + threadIdx.x; i < q_per_head; i += kPlanThreads) qu[i] = BwdUnit{0, 0, 0, 0};
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -570,11 +561,17 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         while (r_cum[et + 1] <= j * 128) ++et;
         const bool whole = r_cum[et + 1] >= j * 128 + 128;
         const int first = r_start[et] + (j * 128 - r_cum[et]);
+        int rows_it[kIters];
+        if (!whole) {
+#pragma unroll
+          for (int it = 0; it < kIters; ++it)
+            if (it * RPI < nrw) rows_it[it] = __shfl_sync(0xffffffffu, it * RPI < 32 ? g0 : g1, (it * RPI + sub) & 31);
+        }
         auto gather = [&](uint32_t dst, const __nv_bfloat16* src) {
 #pragma unroll
           for (int it = 0; it < kIters; ++it) {
             if (it * RPI >= nrw) break;
-            const int g = __shfl_sync(0xffffffffu, it * RPI < 32 ? g0 : g1, (it * RPI + sub) & 31);
+            const int g = rows_it[it];
             cp_async16_zfill(dst + xo[it % kPeriod] + it * RPI * 128, src + static_cast<size_t>(max(g, 0)) * D, g >= 0);
           }
         };
