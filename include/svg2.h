@@ -305,9 +305,9 @@ SVG2_API int svg2_layer_norm(const void* X, int dtype, const float* gamma, const
  *   X, dY  [rows, width] of one type (dtype); dX the same type, out (dX == dY or dX == X: in place).
  *   gamma  float [width], optional (NULL: 1); mean, rstd  float [rows] as svg2_layer_norm wrote them.
  *   dgamma, dbeta  float [width], out, optional.  Sums are float32, in a fixed order: the same on every run.
- *   ws     at least svg2_layer_norm_bwd_workspace_size() bytes, 256-byte aligned (a zeroed status area, as in
- *          every workspace, then the partial sums).
- * Two kernels on `stream`.  Sizes and errors as svg2_layer_norm, and SVG2_ERR_WORKSPACE. */
+ *   ws     at least svg2_layer_norm_bwd_workspace_size() bytes, 256-byte aligned: a status area of 256 bytes
+ *          that must be zero when the workspace is first used, then the partial sums.
+ * One or two kernels on `stream`.  Sizes and errors as svg2_layer_norm, and SVG2_ERR_WORKSPACE. */
 SVG2_API int svg2_layer_norm_bwd_workspace_size(long long rows, int width, size_t* bytes);
 SVG2_API int svg2_layer_norm_bwd(const void* X, const void* dY, int dtype, const float* gamma, const float* mean,
                                  const float* rstd, long long rows, int width, void* dX, float* dgamma,

@@ -495,29 +495,11 @@ int svg2_sparse_attn_fp8(const void* Qp8, const void* Kp8, const void* Vp8, cons
   }
 }
 
-namespace {
-struct DenseCarve {
-  DeviceStatus* st;
-  int32_t *k_off, *sel_count, *sel_idx;
-  AttnScratch attn;
-};
-void carve_dense(Carve& c, int BH, int N, DenseCarve& D) {
-  D.st = c.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
-  D.k_off = c.take<int32_t>(static_cast<size_t>(BH) * 2);
-  D.sel_count = c.take<int32_t>(BH);
-  D.sel_idx = c.take<int32_t>(BH);
-  carve_attn(c, BH, N, 1, D.attn);
-}
-}  // namespace
-
 int svg2_dense_attn_workspace_size(int B, int H, int N, int d, size_t* bytes) {
   if (bytes == nullptr) return SVG2_ERR_INVALID_ARG;
   const int r = check_sizes(B, H, N, d);
   if (r != SVG2_OK) return r;
-  Carve c(nullptr);
-  DenseCarve D;
-  carve_dense(c, B * H, N, D);
-  *bytes = align_up(c.off, 256);
+  *bytes = kStatusBytes;  // dense attention needs no plan
   return SVG2_OK;
 }
 
@@ -528,15 +510,11 @@ static int dense_attn_call(const void* Q, const void* K, const void* V, int B, i
   if (Q == nullptr || K == nullptr || V == nullptr || O == nullptr) return SVG2_ERR_INVALID_ARG;
   if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16)) return SVG2_ERR_INVALID_ARG;
   if (!finite_scale(scale)) return SVG2_ERR_INVALID_ARG;
-  const int BH = B * H;
-  Carve c(ws);
-  DenseCarve D;
-  carve_dense(c, BH, N, D);
-  r = check_ws(ws, ws_bytes, c.off);
+  r = check_ws(ws, ws_bytes, kStatusBytes);
   if (r != SVG2_OK) return r;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return to_status(launch_dense_attn(Q, K, V, BH, N, d, scale, O, lse, D.k_off, D.sel_count, D.sel_idx, D.attn, D.st,
-                                     wait_budget_of(D.st), s));
+  DeviceStatus* st = static_cast<DeviceStatus*>(ws);
+  return to_status(launch_dense_attn(Q, K, V, B * H, N, d, scale, O, lse, st, wait_budget_of(st),
+                                     static_cast<cudaStream_t>(stream)));
 }
 
 int svg2_dense_attn(const void* Q, const void* K, const void* V, int B, int H, int N, int d, float scale, void* O,
@@ -562,13 +540,10 @@ int svg2_dense_attn_lse(const void* Q, const void* K, const void* V, int B, int 
 // (the two calls use it in turn).  nQ = 0: dense.
 static size_t bwd_bytes(int BH, int N, int d, int nQ, int nK, void* ws, DeviceStatus** st, BwdScratch* sc) {
   Carve f(nullptr);
+  f.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
   if (nQ > 0) {
-    f.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
     AttnScratch a;
     carve_attn(f, BH, N, nQ, a);
-  } else {
-    DenseCarve D;
-    carve_dense(f, BH, N, D);
   }
   Carve c(ws);
   DeviceStatus* s = c.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
@@ -707,6 +682,7 @@ int svg2_layer_norm_bwd(const void* X, const void* dY, int dtype, const float* g
     Carve c(ws);
     NormCall n{};
     n.partial = carve_norm(c, rows, width);
+    n.arrived = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kArrivedOffset);
     r = check_ws(ws, ws_bytes, c.off);
     if (r != SVG2_OK) return r;
     n.X = X, n.dY = dY, n.Y = dX, n.gamma = gamma, n.mean = const_cast<float*>(mean);

@@ -127,8 +127,8 @@ __global__ void plan_write_kernel(const int32_t* __restrict__ q_off, int nQ, int
   }
 }
 
-// The three kernels above in one launch, one CTA per (b,h), for plans small enough that each CTA can count the
-// units of all heads before its own: at 40 heads of 100 clusters 4.9 us against 16.4 us for the three.
+// The three kernels above in one launch (the training calls), one CTA per (b,h), for plans small enough that each
+// CTA can count the units of all heads before its own: at 2 heads of 100 clusters 3.8 us against 22.2 us.
 constexpr int kPlanFusedThreads = 256;
 constexpr int kPlanFusedMost = 16384;  // BH * nQ
 
@@ -205,11 +205,17 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                        int nK, float scale, const int32_t* __restrict__ perm_q, __nv_bfloat16* __restrict__ O,
                        float* __restrict__ lse, const AttnUnit* __restrict__ units, const int32_t* __restrict__ head_base, int BH,
                        const F8Scales f8, DeviceStatus* st, const uint64_t* __restrict__ wait_budget) {
-  const int total_units = head_base[BH];
-  if (static_cast<int>(blockIdx.x) >= total_units) return;
+  const bool dense = units == nullptr;  // no plan: every head's rows in order, all N keys
+  if (!dense && static_cast<int>(blockIdx.x) >= head_base[BH]) return;
   if (status_set(st)) return;
   const long long wb = effective_wait_budget(wait_budget);
-  const AttnUnit un = units[blockIdx.x];
+  AttnUnit un;
+  if (dense) {
+    const int per_head = (N + 255) / 256, u = static_cast<int>(blockIdx.x) % per_head;
+    un = AttnUnit{static_cast<int>(blockIdx.x) / per_head, 0, 256 * u, min(256, N - 256 * u)};
+  } else {
+    un = units[blockIdx.x];
+  }
 
   constexpr uint32_t kTile = tile_bytes<D, F8>();
   constexpr int kRowBytes = D * (F8 ? 1 : 2);
@@ -249,7 +255,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
   }
-  if (warp >= kProducerWarp0 && warp < kProducerWarp0 + kProducerWarps) {
+  if (dense) {
+    if (threadIdx.x == 32 * kProducerWarp0) {
+      r_start[0] = r_cum[0] = 0;
+      r_cum[1] = bars->L = N;
+      bars->nranges = 1;
+    }
+  } else if (warp >= kProducerWarp0 && warp < kProducerWarp0 + kProducerWarps) {
     // key-stream range table: start row and stream offset of every kept K cluster
     const int pt = threadIdx.x - 32 * kProducerWarp0;
     const size_t row = static_cast<size_t>(bh) * nQ + un.cluster;
@@ -809,29 +821,6 @@ __global__ void __launch_bounds__(128, 1)
   }
 }
 
-// Dense attention as the one-cluster case: per (b,h) one Q cluster and one K cluster holding all N
-// tokens in their original order, the K cluster selected.  Writes that plan and its work units.
-__global__ void dense_plan_kernel(int BH, int N, int units_per_head, int32_t* __restrict__ k_off,
-                                  int32_t* __restrict__ sel_count, int32_t* __restrict__ sel_idx,
-                                  int32_t* __restrict__ head_base, AttnUnit* __restrict__ units) {
-  const int e = blockIdx.x * blockDim.x + threadIdx.x;
-  const int bh = e / units_per_head, u = e % units_per_head;
-  if (e == 0) head_base[BH] = BH * units_per_head;
-  if (bh >= BH) return;
-  units[e] = AttnUnit{bh, 0, 256 * u, min(256, N - 256 * u)};
-  if (u == 0) {
-    k_off[2 * bh] = 0;
-    k_off[2 * bh + 1] = N;
-    sel_count[bh] = 1;
-    sel_idx[bh] = 0;
-    head_base[bh] = e;
-  }
-}
-
-}  // namespace
-
-namespace {
-
 template <int D, bool F8>
 cudaError_t launch_attn_kernel(const CUtensorMap& tq, const void* Kp, const void* Vp, const int32_t* k_off,
                                const int32_t* sel_count, const int32_t* sel_idx, int BH, int N, int nQ, int nK,
@@ -840,7 +829,7 @@ cudaError_t launch_attn_kernel(const CUtensorMap& tq, const void* Kp, const void
   constexpr uint32_t smem = attn_smem<D, F8>();
   cudaError_t e = cudaFuncSetAttribute(sparse_attn_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const long long grid = static_cast<long long>(BH) * attn_max_units_per_head(N, nQ);
+  const long long grid = static_cast<long long>(BH) * (sc.units != nullptr ? attn_max_units_per_head(N, nQ) : (N + 255) / 256);
   sparse_attn_kernel<D, F8><<<static_cast<unsigned>(grid), kAttnThreads, smem, s>>>(
       tq, static_cast<const AttnElem<F8>*>(Kp), static_cast<const AttnElem<F8>*>(Vp), k_off, sel_count, sel_idx, N, nQ, nK,
       scale, perm_q, static_cast<__nv_bfloat16*>(O), lse, sc.units, sc.head_base, BH, f8, st, wait_budget);
@@ -848,8 +837,8 @@ cudaError_t launch_attn_kernel(const CUtensorMap& tq, const void* Kp, const void
 }
 
 cudaError_t launch_attn_plan(const int32_t* q_off, int BH, int N, int nQ, const AttnScratch& sc, DeviceStatus* st,
-                             cudaStream_t s) {
-  if (static_cast<long long>(BH) * nQ <= kPlanFusedMost) {
+                             cudaStream_t s, bool fused = false) {
+  if (fused && static_cast<long long>(BH) * nQ <= kPlanFusedMost) {
     plan_fused_kernel<<<BH, kPlanFusedThreads, 0, s>>>(q_off, BH, nQ, N, sc.head_base, sc.units,
                                                         BH * attn_max_units_per_head(N, nQ), st);
     return cudaGetLastError();
@@ -864,7 +853,7 @@ cudaError_t launch_attn_plan(const int32_t* q_off, int BH, int N, int nQ, const 
 
 namespace {
 
-// The bf16 attention on a plan whose units are in sc.
+// The bf16 attention on a plan whose units are in sc; without units, dense attention.
 cudaError_t launch_planned(const void* Qp, const void* Kp, const void* Vp, const int32_t* k_off,
                            const int32_t* sel_count, const int32_t* sel_idx, int BH, int N, int d, int nQ, int nK,
                            float scale, const int32_t* perm_q, void* O, float* lse, const AttnScratch& sc,
@@ -886,22 +875,16 @@ cudaError_t launch_sparse_attn(const void* Qp, const void* Kp, const void* Vp, c
                                int N, int d, int nQ, int nK, float scale, const int32_t* perm_q, void* O,
                                const AttnScratch& sc, DeviceStatus* st, const uint64_t* wait_budget,
                                cudaStream_t s, float* lse) {
-  const cudaError_t e = launch_attn_plan(q_off, BH, N, nQ, sc, st, s);
+  const cudaError_t e = launch_attn_plan(q_off, BH, N, nQ, sc, st, s, lse != nullptr);
   if (e != cudaSuccess) return e;
   return launch_planned(Qp, Kp, Vp, k_off, sel_count, sel_idx, BH, N, d, nQ, nK, scale, perm_q, O, lse, sc, st,
                         wait_budget, s);
 }
 
 cudaError_t launch_dense_attn(const void* Q, const void* K, const void* V, int BH, int N, int d, float scale, void* O,
-                              float* lse, int32_t* k_off, int32_t* sel_count, int32_t* sel_idx, const AttnScratch& sc,
-                              DeviceStatus* st, const uint64_t* wait_budget, cudaStream_t s) {
-  const int per_head = (N + 255) / 256;
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(BH) * per_head + 255) / 256);
-  dense_plan_kernel<<<grid, 256, 0, s>>>(BH, N, per_head, k_off, sel_count, sel_idx, sc.head_base, sc.units);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_planned(Q, K, V, k_off, sel_count, sel_idx, BH, N, d, 1, 1, scale, nullptr, O, lse, sc, st, wait_budget,
-                        s);
+                              float* lse, DeviceStatus* st, const uint64_t* wait_budget, cudaStream_t s) {
+  return launch_planned(Q, K, V, nullptr, nullptr, nullptr, BH, N, d, 1, 1, scale, nullptr, O, lse,
+                        AttnScratch{nullptr, nullptr, nullptr}, st, wait_budget, s);
 }
 
 cudaError_t launch_sparse_attn_fp8(const void* Qp8, const void* Kp8, const void* Vp8, const F8Scales& f8,

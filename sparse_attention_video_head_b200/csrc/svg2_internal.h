@@ -52,6 +52,8 @@ enum : uint32_t {
 
 constexpr int kStatusBytes = 256;
 static_assert(kWaitBudgetOffset >= sizeof(DeviceStatus) && kWaitBudgetOffset + 8 <= kStatusBytes, "status area");
+// Counter of the layer norm's gradients (zero between calls, like the rest of a zeroed status area).
+constexpr size_t kArrivedOffset = 32;
 
 // The wait-budget field of the status area that starts at st (a workspace's first bytes).
 inline const uint64_t* wait_budget_of(const DeviceStatus* st) {
@@ -243,6 +245,7 @@ struct NormCall {
   void* Y;                     // Y | dX
   float *dgamma, *dbeta;       // backward, optional
   float* partial;              // backward: [norm_max_parts][2][width]
+  uint32_t* arrived;           // backward: a counter at zero between calls
   long long rows;
   int width;
   float eps;
@@ -277,10 +280,9 @@ cudaError_t launch_gather_e4m3(const void* X0, const void* X1, bool f32, const i
                                const uint32_t* amax0, const uint32_t* amax1, void* Y0, void* Y1, cudaStream_t s,
                                DeviceStatus* st);
 cudaError_t launch_amax_to_scale(uint32_t* amax, int n, cudaStream_t s);
-// Dense attention: one cluster per head (k_off [BH, 2], sel_count and sel_idx [BH] are scratch).
+// Dense attention: the same kernel without a plan, every head's rows in order against all its keys.
 cudaError_t launch_dense_attn(const void* Q, const void* K, const void* V, int BH, int N, int d, float scale, void* O,
-                              float* lse, int32_t* k_off, int32_t* sel_count, int32_t* sel_idx, const AttnScratch& sc,
-                              DeviceStatus* st, const uint64_t* wait_budget, cudaStream_t s);
+                              float* lse, DeviceStatus* st, const uint64_t* wait_budget, cudaStream_t s);
 
 cudaError_t launch_selftest_mma(const void* A, const void* Bm, int n, const void* V, float* C, float* O,
                                 DeviceStatus* st, cudaStream_t s);

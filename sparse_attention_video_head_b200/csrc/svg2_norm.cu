@@ -24,6 +24,9 @@ namespace svg2 {
 
 namespace {
 
+// Up to this many partial values are added by the CTA that comes last, more by a kernel of their own.
+constexpr long long kNormFusedValues = 32768;
+
 template <class T>
 struct NormArgs {
   const T *X, *dY;
@@ -32,6 +35,8 @@ struct NormArgs {
   float *mean, *rstd;              // forward, optional
   T* Y;                            // Y | dX
   float* partial;                  // backward: [gridDim.x][2][W]
+  float *dgamma, *dbeta;           // backward, optional
+  uint32_t* arrived;               // CTAs whose partial row is written, or null: another kernel adds the rows
   long long rows;
   int W;
   int x_mis;               // X's elements past a 16-byte boundary
@@ -447,6 +452,27 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs<T> a) {
       out[c] = s;
     }
   }
+  if (a.arrived == nullptr) return;
+  // Few partial rows: the CTA that comes last adds them up, row by row in order whoever it is, and leaves the
+  // counter at zero for the next call.
+  __shared__ bool last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.arrived, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int c = threadIdx.x; c < 2 * a.W; c += blockDim.x) {
+    float* to = c < a.W ? a.dgamma : a.dbeta;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    int r = 0;
+    for (; r + 4 <= static_cast<int>(gridDim.x); r += 4)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s[u] += __ldcg(a.partial + static_cast<size_t>(r + u) * 2 * a.W + c);
+    for (; r < static_cast<int>(gridDim.x); ++r) s[0] += __ldcg(a.partial + static_cast<size_t>(r) * 2 * a.W + c);
+    if (to != nullptr) to[c < a.W ? c : c - a.W] = (s[0] + s[1]) + (s[2] + s[3]);
+  }
+  if (threadIdx.x == 0) *a.arrived = 0u;
 }
 
 // dgamma, dbeta = the column sums of the partial rows, 32 columns per CTA: warp w adds rows w, w + 32, ...,
@@ -475,7 +501,7 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
 }
 
 template <class T, bool BWD, bool EDGE, int G, int NV, int R, int STAGES, int MAXT>
-cudaError_t run_norm(const NormArgs<T>& a, int threads, int max_parts, int* parts, cudaStream_t s) {
+cudaError_t run_norm(NormArgs<T> a, int threads, int max_parts, int* parts, cudaStream_t s) {
   constexpr int V = kVec<T>;
   constexpr auto kernel =
       BWD ? norm_bwd_kernel<T, EDGE, G, NV, R, STAGES, MAXT> : norm_fwd_kernel<T, EDGE, G, NV, R, STAGES, MAXT>;
@@ -498,6 +524,8 @@ cudaError_t run_norm(const NormArgs<T>& a, int threads, int max_parts, int* part
   if (BWD && grid > max_parts) grid = max_parts;
   if (EDGE && G == 0 && grid < a.rows) grid = std::max(8LL, grid / 8 * 8);  // a CTA's rows are a multiple of 8 apart
   *parts = static_cast<int>(grid);
+  if (BWD && grid * 2 * a.W <= kNormFusedValues) *parts = 0;
+  else a.arrived = nullptr;
   kernel<<<static_cast<unsigned>(grid), threads, smem, s>>>(a);
   return cudaGetLastError();
 }
@@ -543,6 +571,9 @@ cudaError_t run_typed(const NormCall& n, bool bwd, cudaStream_t s) {
   a.rows = n.rows;
   a.W = n.width;
   a.eps = n.eps;
+  a.dgamma = n.dgamma;
+  a.dbeta = n.dbeta;
+  a.arrived = n.arrived;
   auto mis = [](const void* p) { return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T)); };
   a.x_mis = mis(n.X);
   a.dy_same = mis(n.dY) == a.x_mis;
@@ -554,7 +585,7 @@ cudaError_t run_typed(const NormCall& n, bool bwd, cudaStream_t s) {
                               : pick_norm<T, true, false>(a, max_parts, &parts, s))
                       : (edge ? pick_norm<T, false, true>(a, max_parts, &parts, s)
                               : pick_norm<T, false, false>(a, max_parts, &parts, s));
-  if (e == cudaSuccess && bwd && (n.dgamma != nullptr || n.dbeta != nullptr)) {
+  if (e == cudaSuccess && parts > 0 && bwd && (n.dgamma != nullptr || n.dbeta != nullptr)) {
     norm_reduce_kernel<<<(2 * n.width + 31) / 32, 1024, 0, s>>>(n.partial, parts, n.width, n.dgamma, n.dbeta);
     e = cudaGetLastError();
   }
