@@ -411,7 +411,7 @@ static int sparse_attn_call(const void* Qp, const void* Kp, const void* Vp, cons
   Carve c(ws);
   DeviceStatus* st = c.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
   AttnScratch a;
-  carve_attn(c, BH, N, nQ, a);
+  carve_attn(c, BH, N, nQ, a, lse != nullptr);
   r = check_ws(ws, ws_bytes, c.off);
   if (r != SVG2_OK) return r;
   return to_status(launch_sparse_attn(Qp, Kp, Vp, q_off, k_off, sel_count, sel_idx, BH, N, d, nQ, nK, scale, perm_q, O,
@@ -543,7 +543,7 @@ static size_t bwd_bytes(int BH, int N, int d, int nQ, int nK, void* ws, DeviceSt
   f.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));
   if (nQ > 0) {
     AttnScratch a;
-    carve_attn(f, BH, N, nQ, a);
+    carve_attn(f, BH, N, nQ, a, true);
   }
   Carve c(ws);
   DeviceStatus* s = c.take<DeviceStatus>(kStatusBytes / sizeof(DeviceStatus));

@@ -133,7 +133,7 @@ constexpr int kPlanFusedThreads = 256;
 constexpr int kPlanFusedMost = 16384;  // BH * nQ
 
 __global__ void __launch_bounds__(kPlanFusedThreads)
-    plan_fused_kernel(const int32_t* __restrict__ q_off, int BH, int nQ, int N, int32_t* __restrict__ head_base,
+    plan_fused_kernel(const int32_t* __restrict__ q_off, int BH, int nQ, int N, int unit, int32_t* __restrict__ head_base,
                       AttnUnit* __restrict__ units, int most, DeviceStatus* st) {
   __shared__ int32_t part[kPlanFusedThreads / 32];
   const int bh = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kPlanFusedThreads)
     const int32_t* qo = q_off + static_cast<size_t>(b) * (nQ + 1) + i;
     r0 = qo[0];
     n = qo[1] - r0;
-    return (r0 < 0 || n <= 0 || r0 + n > N) ? 0 : (n + 255) / 256;  // malformed offsets produce no work
+    return (r0 < 0 || n <= 0 || r0 > N - n) ? 0 : (n + unit - 1) / unit;  // malformed offsets produce no work
   };
   auto block_sum = [&](int v) {
 #pragma unroll
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kPlanFusedThreads)
       if (w < warp) pos += part[w];
       total += part[w];
     }
-    for (int k = 0; k < u && pos + k < most; ++k) units[pos + k] = AttnUnit{bh, i, r0 + 256 * k, min(256, n - 256 * k)};
+    for (int k = 0; k < u && pos + k < most; ++k) units[pos + k] = AttnUnit{bh, i, r0 + unit * k, min(unit, n - unit * k)};
     run += total;
     __syncthreads();
   }
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const long long wb = effective_wait_budget(wait_budget);
   AttnUnit un;
   if constexpr (dense) {
-    const int per_head = (N + 255) / 256, u = static_cast<int>(blockIdx.x) % per_head;
-    un = AttnUnit{static_cast<int>(blockIdx.x) / per_head, 0, 256 * u, min(256, N - 256 * u)};
+    const int per_head = (N + nQ - 1) / nQ, u = static_cast<int>(blockIdx.x) % per_head;  // nQ: rows of a unit
+    un = AttnUnit{static_cast<int>(blockIdx.x) / per_head, 0, nQ * u, min(nQ, N - nQ * u)};
   } else {
     un = units[blockIdx.x];
   }
@@ -839,7 +839,9 @@ cudaError_t launch_attn_kernel(const CUtensorMap& tq, const void* Kp, const void
   auto* kernel = sparse_attn_kernel<D, F8, MODE>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const long long per_head = MODE == AttnMode::kDense ? (N + 255) / 256 : attn_max_units_per_head(N, nQ);
+  const long long per_head = MODE == AttnMode::kDense     ? (N + nQ - 1) / nQ
+                             : MODE == AttnMode::kPlanLse ? attn_lse_units_per_head(BH, N, nQ)
+                                                          : attn_max_units_per_head(N, nQ);
   kernel<<<static_cast<unsigned>(BH * per_head), kAttnThreads, smem, s>>>(
       tq, static_cast<const AttnElem<F8>*>(Kp), static_cast<const AttnElem<F8>*>(Vp), k_off, sel_count, sel_idx, N, nQ, nK,
       scale, perm_q, static_cast<__nv_bfloat16*>(O), lse, sc.units, sc.head_base, BH, f8, st, wait_budget);
@@ -847,10 +849,10 @@ cudaError_t launch_attn_kernel(const CUtensorMap& tq, const void* Kp, const void
 }
 
 cudaError_t launch_attn_plan(const int32_t* q_off, int BH, int N, int nQ, const AttnScratch& sc, DeviceStatus* st,
-                             cudaStream_t s, bool fused = false) {
-  if (fused && static_cast<long long>(BH) * nQ <= kPlanFusedMost) {
-    plan_fused_kernel<<<BH, kPlanFusedThreads, 0, s>>>(q_off, BH, nQ, N, sc.head_base, sc.units,
-                                                        BH * attn_max_units_per_head(N, nQ), st);
+                             cudaStream_t s, bool with_lse = false) {
+  if (with_lse && static_cast<long long>(BH) * nQ <= kPlanFusedMost) {
+    plan_fused_kernel<<<BH, kPlanFusedThreads, 0, s>>>(q_off, BH, nQ, N, attn_unit_rows(BH, N), sc.head_base, sc.units,
+                                                        BH * attn_lse_units_per_head(BH, N, nQ), st);
     return cudaGetLastError();
   }
   plan_count_kernel<<<BH, 256, 0, s>>>(q_off, nQ, N, sc.head_units, st);
@@ -897,8 +899,8 @@ cudaError_t launch_sparse_attn(const void* Qp, const void* Kp, const void* Vp, c
 
 cudaError_t launch_dense_attn(const void* Q, const void* K, const void* V, int BH, int N, int d, float scale, void* O,
                               float* lse, DeviceStatus* st, const uint64_t* wait_budget, cudaStream_t s) {
-  return launch_bf16<AttnMode::kDense>(Q, K, V, nullptr, nullptr, nullptr, BH, N, d, 1, 1, scale, nullptr, O, lse,
-                                       AttnScratch{nullptr, nullptr, nullptr}, st, wait_budget, s);
+  return launch_bf16<AttnMode::kDense>(Q, K, V, nullptr, nullptr, nullptr, BH, N, d, attn_unit_rows(BH, N), 1, scale, nullptr, O,
+                                       lse, AttnScratch{nullptr, nullptr, nullptr}, st, wait_budget, s);
 }
 
 cudaError_t launch_sparse_attn_fp8(const void* Qp8, const void* Kp8, const void* Vp8, const F8Scales& f8,

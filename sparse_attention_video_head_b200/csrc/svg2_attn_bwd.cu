@@ -142,7 +142,8 @@ __device__ void mean_key(const uint4* __restrict__ K, int bh, int N, float* __re
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 16
   for (int t = group; t < S; t += kGroups) {
-    const long long row = static_cast<long long>(bh) * N + static_cast<long long>(t) * N / S;
+    // floor(t N / S) without a 64-bit division
+    const long long row = static_cast<long long>(bh) * N + t * (N / S) + static_cast<int>(static_cast<unsigned>(t * (N % S)) / static_cast<unsigned>(S));
     const uint4 w = __ldg(K + row * kLanes + sub);
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -176,44 +177,56 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
     mean_key<D>(K, blockIdx.x, N, k_mean);
     return;
   }
-  constexpr int kLanes = D / 8;
+  constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes, kUnroll = 2;
   const int sub = threadIdx.x % kLanes;
-  const long long step = static_cast<long long>(gridDim.x - BH) * (256 / kLanes);
-  const long long first = static_cast<long long>(blockIdx.x - BH) * (256 / kLanes) + threadIdx.x / kLanes;
+  const unsigned total = static_cast<unsigned>(rows);  // below 2^31
+  const unsigned step = (gridDim.x - BH) * 8u * kPerWarp;
   // every lane of a warp takes part in the shuffles: rows past the end only skip their memory
-  for (long long r0 = first - (threadIdx.x % 32) / kLanes; r0 < rows; r0 += step) {
-    const long long r = r0 + (threadIdx.x % 32) / kLanes;
-    const bool in = r < rows;
-    long long src = r;
-    bool valid = in;
-    if (in && perm != nullptr) {
-      const long long bh = r / N;
-      const int t = perm[r];
-      SVG2_DEBUG_CHECK(t >= 0 && t < N, st, kWhereGather, r, t);
-      valid = t >= 0 && t < N;  // a bad entry has no output row, so no gradient either
-      src = bh * N + t;
-    }
-    uint4 o = make_uint4(0, 0, 0, 0), g = make_uint4(0, 0, 0, 0);
-    if (valid) {
-      o = O[src * kLanes + sub];
-      g = dO[src * kLanes + sub];
-    }
-    float acc = 0.f;
-    const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
+  for (unsigned r0 = ((blockIdx.x - BH) * 8u + threadIdx.x / 32) * kPerWarp; r0 < total; r0 += kUnroll * step) {
+    uint4 o[kUnroll], g[kUnroll];
+    float l[kUnroll];
+    unsigned src[kUnroll];
+    bool valid[kUnroll];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      acc = fmaf(bf16lo_to_f32(ow[e]), bf16lo_to_f32(gw[e]), acc);
-      acc = fmaf(bf16hi_to_f32(ow[e]), bf16hi_to_f32(gw[e]), acc);
+    for (int u = 0; u < kUnroll; ++u) {
+      const unsigned r = r0 + u * step + (threadIdx.x % 32) / kLanes;
+      valid[u] = r < total;
+      src[u] = r;
+      if (valid[u] && perm != nullptr) {
+        const int t = perm[r];
+        SVG2_DEBUG_CHECK(t >= 0 && t < N, st, kWhereGather, r, t);
+        valid[u] = t >= 0 && t < N;  // a bad entry has no output row, so no gradient either
+        src[u] = r / static_cast<unsigned>(N) * static_cast<unsigned>(N) + t;
+      }
+      l[u] = r < total && sub == 0 ? lse[r] : 0.f;
     }
 #pragma unroll
-    for (int s = kLanes / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
-    if (in) {
-      if (dOp != nullptr) dOp[r * kLanes + sub] = g;
+    for (int u = 0; u < kUnroll; ++u) {
+      o[u] = g[u] = make_uint4(0, 0, 0, 0);
+      if (valid[u]) {
+        o[u] = O[static_cast<size_t>(src[u]) * kLanes + sub];
+        g[u] = dO[static_cast<size_t>(src[u]) * kLanes + sub];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const unsigned r = r0 + u * step + (threadIdx.x % 32) / kLanes;
+      float acc = 0.f;
+      const uint32_t ow[4] = {o[u].x, o[u].y, o[u].z, o[u].w}, gw[4] = {g[u].x, g[u].y, g[u].z, g[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc = fmaf(bf16lo_to_f32(ow[e]), bf16lo_to_f32(gw[e]), acc);
+        acc = fmaf(bf16hi_to_f32(ow[e]), bf16hi_to_f32(gw[e]), acc);
+      }
+#pragma unroll
+      for (int s = kLanes / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
+      if (r >= total) continue;
+      if (dOp != nullptr) dOp[static_cast<size_t>(r) * kLanes + sub] = g[u];
       if (sub == 0) {
-        const float l = lse[r];
-        neg_lse2[r] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row without keys has P = 0
+        const bool empty = l[u] == -INFINITY;  // a row without keys: P = 0 (and it is in no stream)
+        neg_lse2[r] = empty ? -INFINITY : -l[u] * kLog2e;
         neg_delta[r] = -acc;
-        lse_step[r] = three_bf16(l == -INFINITY ? 0.f : -l * inv_scale);  // (such a row is in no stream)
+        lse_step[r] = three_bf16(empty ? 0.f : -l[u] * inv_scale);
         delta_step[r] = three_bf16(-acc);
       }
     }
@@ -229,7 +242,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
 // rarely end on a multiple of 128.  So what is left of a cluster after its full tiles shares a unit with the
 // rows that follow; the joint stream is the union of the clusters' streams, and the pairs that a row's own
 // cluster does not keep are masked.  On 8 heads of 12480 tokens in 64 / 256 clusters (49 rows per K cluster),
-// 60 % kept, units of one cluster each took 2.91 ms, shared ones MEASURE.
+// 60 % kept, the gradients took 2.91 ms with units of one cluster each and take 1.81 ms.
 // ------------------------------------------------------------------------------------------------
 
 // One warp packs clusters [c0, c1) into units, lane w holding word w of the clusters' bits; lane 0 calls

@@ -128,14 +128,25 @@ struct AttnUnit {
 
 inline int attn_max_units_per_head(int N, int nQ) { return (N + 255) / 256 + nQ; }
 
+// Rows of a unit of dense attention and of the attention with log-sum-exp: one Q tile where units of two would
+// leave half of the 148 SMs without work (6 heads of 1333 tokens, d = 64: 15.9 us against 25.7), else two.
+inline int attn_unit_rows(int BH, int N) {
+  return static_cast<long long>(BH) * ((N + 255) / 256) <= 74 ? 128 : 256;
+}
+// (at most this many per head; a plan too large for the one-launch plan kernel has more planes than that)
+inline int attn_lse_units_per_head(int BH, int N, int nQ) {
+  const int rows = attn_unit_rows(BH, N);
+  return (N + rows - 1) / rows + nQ;
+}
+
 struct AttnScratch {
   AttnUnit* units;     // [BH * max_units_per_head] compacted
   int32_t* head_units; // [BH]
   int32_t* head_base;  // [BH + 1]
 };
 
-inline void carve_attn(Carve& c, int BH, int N, int nQ, AttnScratch& s) {
-  s.units = c.take<AttnUnit>(static_cast<size_t>(BH) * attn_max_units_per_head(N, nQ));
+inline void carve_attn(Carve& c, int BH, int N, int nQ, AttnScratch& s, bool with_lse = false) {
+  s.units = c.take<AttnUnit>(static_cast<size_t>(BH) * (with_lse ? attn_lse_units_per_head(BH, N, nQ) : attn_max_units_per_head(N, nQ)));
   s.head_units = c.take<int32_t>(BH);
   s.head_base = c.take<int32_t>(BH + 1);
 }
