@@ -43,6 +43,7 @@ static_assert(256 * kBwdSoftmaxRegs + (kBwdThreads - 256) * kBwdOtherRegs <= kBw
               "register split");
 constexpr int kBwdMmaWarp = 8, kBwdProducerWarp = 9;
 constexpr int kBwdMaxRanges = 1024;
+constexpr uint32_t kGatherSleep = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 // Of every 16 column pairs, this many get 2^x from the cubic on the FMA pipe, the rest from the MUFU: P and dS
 // follow one another in the same warps, so the exponentials' time counts in full (2 x 50000 x 128: 7.32 ms
@@ -64,10 +65,15 @@ constexpr uint32_t kStepBytes = 4096, kStepPlane = 2048;
 constexpr int kBwdMaxSegments = 12;
 constexpr uint32_t kSegPenalty = 0xff7fu;  // bf16 -3.39e38
 
+// Stages of the streamed tiles: four tiles fit at d = 128.  T1 waits from its S product to the unit's last product
+// of the tile, T2 only from dP (to dV), so three and one let T1 arrive a period early: 8 x 12480 x 128 takes 1.75 ms
+// against 1.92 with two of each.  (At d = 64 more would fit; four of each gained nothing.)
+constexpr int kStages1 = 3, kStages2 = 1, kStreamTiles = kStages1 + kStages2;
+
 template <int D>
 constexpr uint32_t bwd_smem() {
-  return 6 * bwd_tile_bytes<D>() + 1024 /*align*/ + 2048 /*row sums*/ + 4096 /*range starts*/ +
-         4096 + 64 /*range offsets*/ + 2048 /*range segments*/ + 5 * kStepBytes /*A, B of S and dP by stage*/ +
+  return (2 + kStreamTiles) * bwd_tile_bytes<D>() + 1024 /*align*/ + 2048 /*row sums*/ + 4096 /*range starts*/ +
+         4096 + 64 /*range offsets*/ + 2048 /*range segments*/ + (1 + kStreamTiles) * kStepBytes /*A, B of S and dP by stage*/ +
          256 /*barriers*/;
 }
 static_assert(bwd_smem<128>() <= 227 * 1024, "shared memory");
@@ -119,7 +125,7 @@ struct BwdArgs {
 };
 
 struct BwdBars {
-  uint64_t res_full, t1_full[2], t2_full[2], t1_empty[2], t2_empty[2], s_full[2], p_full[2], dp_full, ds_full[2], o_full,
+  uint64_t res_full, t1_full[kStages1], t2_full[kStages2], t1_empty[kStages1], t2_empty[kStages2], s_full[2], p_full[2], dp_full, ds_full[2], o_full,
       mma_done;
   uint32_t tmem_base;
   int32_t L, nranges;
@@ -392,19 +398,20 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
   constexpr int kHalves = D / 64;   // 128-byte swizzle atoms across a row
   constexpr int kSteps = D / 16;    // instructions of one S or dP product
   using Tm = BwdTmem<KV>;
+  constexpr int S1 = kStages1, S2 = kStages2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t tmem = bars->tmem_base;
   const int L = bars->L;
   const int T = (L + 127) / 128;
   DeviceStatus* st = a.st;
-  const uint32_t r1 = smem_u32(smem), r2 = r1 + kTile, t1 = r1 + 2 * kTile, t2 = r1 + 4 * kTile;
+  const uint32_t r1 = smem_u32(smem), r2 = r1 + kTile, t1 = r1 + 2 * kTile, t2 = t1 + S1 * kTile;
 
   if (warp == kBwdMmaWarp) {
     if (elect_one() && T > 0) {
       const uint32_t id_s = idesc_bf16_f32(128, 128, 0);  // both operands K-major
       const uint32_t id_o = idesc_bf16_f32(128, D, 1);    // B = a streamed tile read row-major (MN-major)
       // D[slot] = R x T^T, contraction over d, and the step's columns (B at `step`, 0: none)
-      const uint32_t step_a = smem_u32(step_s), step_b = step_a + kStepBytes;  // B of S, dP of stage 0, then of stage 1
+      const uint32_t step_a = smem_u32(step_s), step_b = step_a + kStepBytes;  // B of S by stage of T1, then of dP by stage of T2
       auto product = [&](uint32_t d_tmem, uint32_t ra, uint32_t tb, uint32_t step) {
         const uint64_t da = sdesc_sw128(ra, 16, 1024), db = sdesc_sw128(tb, 16, 1024);
 #pragma unroll
@@ -415,8 +422,8 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         if (step != 0u)
           mma_ss(d_tmem, sdesc_plain(step_a, kStepPlane, 128), sdesc_plain(step, kStepPlane, 128), id_s, 1u);
       };
-      auto s_step = [&](int stage) { return KV || MULTI ? step_b + stage * 2 * kStepBytes : 0u; };
-      auto dp_step = [&](int stage) { return KV ? step_b + (stage * 2 + 1) * kStepBytes : 0u; };
+      auto s_step = [&](int stage) { return KV || MULTI ? step_b + stage * kStepBytes : 0u; };
+      auto dp_step = [&](int stage) { return KV ? step_b + (S1 + stage) * kStepBytes : 0u; };
       // acc (+)= X T with X (P or dS, bf16) in TMEM, contraction over the tile's 128 rows, in the two chunks in
       // which X is handed over: rows 0-31 and 64-95, then 32-63 and 96-127
       auto accumulate = [&](uint32_t acc, uint32_t x, uint32_t tb, int chunk, bool add) {
@@ -449,8 +456,9 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         mma_commit(smem_u32(&bars->dp_full));
         if (!KV) mma_commit(smem_u32(&bars->t2_empty[0]));
       }
+      // stage and phase of tile j + 1 (c1, c2: of tile j)
+      int c1 = 0, c2 = 0, g1 = S1 > 1 ? 1 : 0, g2 = S2 > 1 ? 1 : 0, ph1 = S1 > 1 ? 0 : 1, ph2 = S2 > 1 ? 0 : 1;
       for (int j = 0; j < T && ok; ++j) {
-        const int sg = j & 1, ng = sg ^ 1;
         const bool more = j + 1 < T;
         if constexpr (KV) {
 #pragma unroll
@@ -458,38 +466,43 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
             if (ok) ok = wait(&bars->p_full[c], j);
             if (!ok) break;
             tc_fence_after();
-            accumulate(tmem + Tm::acc1, tmem, t2 + sg * kTile, c, j > 0 || c > 0);  // dV += P^T dO
+            accumulate(tmem + Tm::acc1, tmem, t2 + c2 * kTile, c, j > 0 || c > 0);  // dV += P^T dO
           }
           if (!ok) break;
-          mma_commit(smem_u32(&bars->t2_empty[sg]));
+          mma_commit(smem_u32(&bars->t2_empty[c2]));
         }
         if (more) {
           // key unit: the products run in issue order, so S(j+1) overwrites P(j) only after dV has read it;
           // query unit: the other slot, whose S(j-1) was read before dS(j-1) was handed over
-          ok = wait_tile(&bars->t1_full[ng], (j + 1) >> 1);
+          ok = wait_tile(&bars->t1_full[g1], ph1);
           if (!ok) break;
           tc_fence_after();
-          product(tmem + (KV ? 0u : ng * Tm::s1), r1, t1 + ng * kTile, s_step(ng));
-          mma_commit(smem_u32(&bars->s_full[KV ? 0 : ng]));
+          const int slot = KV ? 0 : (j + 1) & 1;
+          product(tmem + slot * Tm::s1, r1, t1 + g1 * kTile, s_step(g1));
+          mma_commit(smem_u32(&bars->s_full[slot]));
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           if (ok) ok = wait(&bars->ds_full[c], j);
           if (!ok) break;
           tc_fence_after();
-          accumulate(tmem + Tm::acc2, tmem + Tm::dp, t1 + sg * kTile, c, j > 0 || c > 0);  // dK += dS^T Q | dQ += dS K
-          if constexpr (SPLIT) accumulate(tmem + Tm::acc2, tmem + Tm::dp + 32, t1 + sg * kTile, c, true);
+          accumulate(tmem + Tm::acc2, tmem + Tm::dp, t1 + c1 * kTile, c, j > 0 || c > 0);  // dK += dS^T Q | dQ += dS K
+          if constexpr (SPLIT) accumulate(tmem + Tm::acc2, tmem + Tm::dp + 32, t1 + c1 * kTile, c, true);
         }
         if (!ok) break;
-        mma_commit(smem_u32(&bars->t1_empty[sg]));
+        mma_commit(smem_u32(&bars->t1_empty[c1]));
         if (more) {
-          ok = wait_tile(&bars->t2_full[ng], (j + 1) >> 1);
+          ok = wait_tile(&bars->t2_full[g2], ph2);
           if (!ok) break;
           tc_fence_after();
-          product(tmem + Tm::dp, r2, t2 + ng * kTile, dp_step(ng));
+          product(tmem + Tm::dp, r2, t2 + g2 * kTile, dp_step(g2));
           mma_commit(smem_u32(&bars->dp_full));
-          if (!KV) mma_commit(smem_u32(&bars->t2_empty[ng]));
+          if (!KV) mma_commit(smem_u32(&bars->t2_empty[g2]));
         }
+        c1 = g1;
+        c2 = g2;
+        if (++g1 == S1) g1 = 0, ph1 ^= 1;
+        if (++g2 == S2) g2 = 0, ph2 ^= 1;
       }
       if (ok) mma_commit(smem_u32(&bars->o_full));
       mma_commit(smem_u32(&bars->mma_done));
@@ -520,33 +533,36 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       for (int h = 0; h < kHalves; ++h) tma_load_3d(dst + h * 16384, m, h * 64, row, bh, bar);
     };
     const size_t plane = static_cast<size_t>(bh) * a.N;
-    const uint32_t step_b = smem_u32(step_s) + kStepBytes;  // B of S, dP of stage 0, then of stage 1
+    const uint32_t step_b = smem_u32(step_s) + kStepBytes;  // B of S by stage of T1, then of dP by stage of T2
     int n1 = 0, n2 = 0;  // tiles requested of each streamed operand
     bool ok = true;
-    auto wait_empty = [&](uint64_t* bar, int j) {
-      return j < 2 || __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(bar), ((j >> 1) - 1) & 1, st,
-                                                              kWhereAttnBwdProducer, 100, wb));
+    // `round`: how often the stage was filled before
+    auto wait_empty = [&](uint64_t* bar, int round) {
+      return round == 0 || __all_sync(0xffffffffu, mbar_wait_sleep(smem_u32(bar), (round - 1) & 1, st,
+                                                                   kWhereAttnBwdProducer, DENSE ? 100 : kGatherSleep, wb));
     };
+    int g1 = 0, g2 = 0, round1 = 0, round2 = 0;  // stage of tile j and its round
     if constexpr (DENSE) {
       for (int j = 0; j < T; ++j) {
-        const int sg = j & 1;
-        const uint32_t b1 = smem_u32(&bars->t1_full[sg]), b2 = smem_u32(&bars->t2_full[sg]);
+        const uint32_t b1 = smem_u32(&bars->t1_full[g1]), b2 = smem_u32(&bars->t2_full[g2]);
         // the rows' step operands: as many as the plane still has (columns past it are masked)
         const uint32_t bytes = KV ? min(128, a.N - j * 128) * 16u : 0u;
-        ok = wait_empty(&bars->t1_empty[sg], j);
+        ok = wait_empty(&bars->t1_empty[g1], round1);
         if (!ok) break;
         if (leader) {
-          tma_tile(m1, t1 + sg * kTile, b1, j * 128, bytes);
-          if (KV) bulk_load(step_b + sg * 2 * kStepBytes, a.lse_step + plane + j * 128, bytes, b1);
+          tma_tile(m1, t1 + g1 * kTile, b1, j * 128, bytes);
+          if (KV) bulk_load(step_b + g1 * kStepBytes, a.lse_step + plane + j * 128, bytes, b1);
         }
         n1 = j + 1;
-        ok = wait_empty(&bars->t2_empty[sg], j);
+        ok = wait_empty(&bars->t2_empty[g2], round2);
         if (!ok) break;
         if (leader) {
-          tma_tile(m2, t2 + sg * kTile, b2, j * 128, bytes);
-          if (KV) bulk_load(step_b + (sg * 2 + 1) * kStepBytes, a.delta_step + plane + j * 128, bytes, b2);
+          tma_tile(m2, t2 + g2 * kTile, b2, j * 128, bytes);
+          if (KV) bulk_load(step_b + (S1 + g2) * kStepBytes, a.delta_step + plane + j * 128, bytes, b2);
         }
         n2 = j + 1;
+        if (++g1 == S1) g1 = 0, ++round1;
+        if (++g2 == S2) g2 = 0, ++round2;
       }
     } else {
       constexpr int CPR = D / 8;           // 16-byte chunks per row
@@ -568,9 +584,8 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         return r_start[e] + (p - r_cum[e]);
       };
       for (int j = 0; j < T; ++j) {
-        const int sg = j & 1;
-        const uint32_t b1 = smem_u32(&bars->t1_full[sg]), b2 = smem_u32(&bars->t2_full[sg]);
-        const int g0 = src_row(j * 128 + wr0 + lane, e0), g1 = src_row(j * 128 + wr0 + 32 + lane, e1);
+        const uint32_t b1 = smem_u32(&bars->t1_full[g1]), b2 = smem_u32(&bars->t2_full[g2]);
+        const int ra = src_row(j * 128 + wr0 + lane, e0), rb = src_row(j * 128 + wr0 + 32 + lane, e1);
         while (r_cum[et + 1] <= j * 128) ++et;
         const bool whole = r_cum[et + 1] >= j * 128 + 128;
         const int first = r_start[et] + (j * 128 - r_cum[et]);
@@ -578,59 +593,61 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         if (!whole) {
 #pragma unroll
           for (int it = 0; it < kIters; ++it)
-            if (it * RPI < nrw) rows_it[it] = __shfl_sync(0xffffffffu, it * RPI < 32 ? g0 : g1, (it * RPI + sub) & 31);
+            if (it * RPI < nrw) rows_it[it] = __shfl_sync(0xffffffffu, it * RPI < 32 ? ra : rb, (it * RPI + sub) & 31);
         }
         auto gather = [&](uint32_t dst, const __nv_bfloat16* src) {
 #pragma unroll
           for (int it = 0; it < kIters; ++it) {
             if (it * RPI >= nrw) break;
-            const int g = rows_it[it];
-            cp_async16_zfill(dst + xo[it % kPeriod] + it * RPI * 128, src + static_cast<size_t>(max(g, 0)) * D, g >= 0);
+            const int r = rows_it[it];
+            cp_async16_zfill(dst + xo[it % kPeriod] + it * RPI * 128, src + static_cast<size_t>(max(r, 0)) * D, r >= 0);
           }
         };
-        ok = wait_empty(&bars->t1_empty[sg], j);
+        ok = wait_empty(&bars->t1_empty[g1], round1);
         if (!ok) break;
         if (whole) {
-          if (leader) tma_tile(m1, t1 + sg * kTile, b1, first, 0u);
+          if (leader) tma_tile(m1, t1 + g1 * kTile, b1, first, 0u);
         } else {
           if (leader) mbar_arrive(b1);
-          gather(t1 + sg * kTile, s1);
+          gather(t1 + g1 * kTile, s1);
         }
         // a stream row's step operand: of the query (key unit), then its segments (MULTI; 8 bytes hold the three bf16)
-        auto row_step = [&](uint32_t dst, const uint4* src, int c, int g) {
-          const uint4* from = src + plane + max(g, 0);
-          if (MULTI) cp_async8_zfill(dst + c * 16, from, g >= 0);
-          else cp_async16_zfill(dst + c * 16, from, g >= 0);
+        auto row_step = [&](uint32_t dst, const uint4* src, int c, int r) {
+          const uint4* from = src + plane + max(r, 0);
+          if (MULTI) cp_async8_zfill(dst + c * 16, from, r >= 0);
+          else cp_async16_zfill(dst + c * 16, from, r >= 0);
         };
         if constexpr (KV) {
-          row_step(step_b + sg * 2 * kStepBytes, a.lse_step, wr0 + lane, g0);
-          if (32 + lane < nrw) row_step(step_b + sg * 2 * kStepBytes, a.lse_step, wr0 + 32 + lane, g1);
+          row_step(step_b + g1 * kStepBytes, a.lse_step, wr0 + lane, ra);
+          if (32 + lane < nrw) row_step(step_b + g1 * kStepBytes, a.lse_step, wr0 + 32 + lane, rb);
         }
         cp_async_mbar_arrive(b1);
         if constexpr (MULTI) {  // (plain stores: an arrival of their own orders them)
-          auto segs = [&](int c, int g, int e) {
-            if (g >= 0) store_seg(step_s + (1 + sg * 2) * kStepBytes, c, r_seg[e]);
+          auto segs = [&](int c, int r, int e) {
+            if (r >= 0) store_seg(step_s + (1 + g1) * kStepBytes, c, r_seg[e]);
           };
-          segs(wr0 + lane, g0, e0);
-          if (32 + lane < nrw) segs(wr0 + 32 + lane, g1, e1);
+          segs(wr0 + lane, ra, e0);
+          if (32 + lane < nrw) segs(wr0 + 32 + lane, rb, e1);
           fence_proxy_async_smem();
         }
         mbar_arrive(b1);
         n1 = j + 1;
-        ok = wait_empty(&bars->t2_empty[sg], j);
+        ok = wait_empty(&bars->t2_empty[g2], round2);
         if (!ok) break;
         if (whole) {
-          if (leader) tma_tile(m2, t2 + sg * kTile, b2, first, 0u);
+          if (leader) tma_tile(m2, t2 + g2 * kTile, b2, first, 0u);
         } else {
           if (leader) mbar_arrive(b2);
-          gather(t2 + sg * kTile, s2);
+          gather(t2 + g2 * kTile, s2);
         }
         if constexpr (KV) {
-          row_step(step_b + (sg * 2 + 1) * kStepBytes, a.delta_step, wr0 + lane, g0);
-          if (32 + lane < nrw) row_step(step_b + (sg * 2 + 1) * kStepBytes, a.delta_step, wr0 + 32 + lane, g1);
+          row_step(step_b + (S1 + g2) * kStepBytes, a.delta_step, wr0 + lane, ra);
+          if (32 + lane < nrw) row_step(step_b + (S1 + g2) * kStepBytes, a.delta_step, wr0 + 32 + lane, rb);
         }
         cp_async_mbar_arrive(b2);
         n2 = j + 1;
+        if (++g1 == S1) g1 = 0, ++round1;
+        if (++g2 == S2) g2 = 0, ++round2;
       }
     }
     // Every copy has landed before the CTA leaves, also when some agent gave up: the last phase of each
@@ -639,12 +656,12 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
     if (leader && T > 0) {
       const long long drain = kWaitBudgetCycles / 8;
       mbar_wait(smem_u32(&bars->res_full), 0, nullptr, kWhereAttnBwdProducer, drain);
-#pragma unroll
-      for (int sg = 0; sg < 2; ++sg) {
-        const int f1 = (n1 + 1 - sg) >> 1, f2 = (n2 + 1 - sg) >> 1;  // fills of this stage
-        if (f1 > 0) mbar_wait(smem_u32(&bars->t1_full[sg]), (f1 - 1) & 1, nullptr, kWhereAttnBwdProducer, drain);
-        if (f2 > 0) mbar_wait(smem_u32(&bars->t2_full[sg]), (f2 - 1) & 1, nullptr, kWhereAttnBwdProducer, drain);
-      }
+      for (int g = 0; g < S1; ++g)
+        if (const int fills = (n1 + S1 - 1 - g) / S1; fills > 0)
+          mbar_wait(smem_u32(&bars->t1_full[g]), (fills - 1) & 1, nullptr, kWhereAttnBwdProducer, drain);
+      for (int g = 0; g < S2; ++g)
+        if (const int fills = (n2 + S2 - 1 - g) / S2; fills > 0)
+          mbar_wait(smem_u32(&bars->t2_full[g]), (fills - 1) & 1, nullptr, kWhereAttnBwdProducer, drain);
     }
   } else if (warp < 8) {
     // ---------------- P and dS, then the unit's rows of the gradients ----------------
@@ -675,9 +692,8 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
     // Every tile goes in two chunks of 32 columns: the loads of the second run under the first's arithmetic, and
     // the MMA warp starts on the first while the second is computed.
     for (int j = 0; j < T; ++j) {
-      const int sg = j & 1;
-      ok = KV ? wait(&bars->s_full[0], j) : wait(&bars->s_full[sg], j >> 1);
-      const uint32_t t_s = tmem + lane_off + (KV ? 0u : sg * Tm::s1) + half * 64;
+      ok = KV ? wait(&bars->s_full[0], j) : wait(&bars->s_full[j & 1], j >> 1);
+      const uint32_t t_s = tmem + lane_off + (KV ? 0u : (j & 1) * Tm::s1) + half * 64;
       const uint32_t t_dp = tmem + lane_off + Tm::dp + half * 64;
       uint32_t sv[64];
       float2 p[32];
@@ -926,22 +942,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   constexpr uint32_t kTile = bwd_tile_bytes<D>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* stats = reinterpret_cast<float*>(smem + 6 * kTile);  // sums over rows' halves, or columns
+  float* stats = reinterpret_cast<float*>(smem + (2 + kStreamTiles) * kTile);  // sums over rows' halves, or columns
   int32_t* r_start = reinterpret_cast<int32_t*>(stats + 512);
   int32_t* r_cum = r_start + kBwdMaxRanges;  // kBwdMaxRanges + 1 entries
   uint16_t* r_seg = reinterpret_cast<uint16_t*>(r_cum + kBwdMaxRanges + 16);
-  uint8_t* step_s = reinterpret_cast<uint8_t*>(r_seg + kBwdMaxRanges);  // A, then B of S and of dP for both stages
-  BwdBars* bars = reinterpret_cast<BwdBars*>(step_s + 5 * kStepBytes);
+  uint8_t* step_s = reinterpret_cast<uint8_t*>(r_seg + kBwdMaxRanges);  // A, then B of S and of dP by stage
+  BwdBars* bars = reinterpret_cast<BwdBars*>(step_s + (1 + kStreamTiles) * kStepBytes);
   const int warp = threadIdx.x >> 5;
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&bars->res_full), 1);
-    for (int i = 0; i < 2; ++i) {
-      // the TMA bytes (or the leader's arrival); when sparse, each producer lane's own copies and plain stores
+    // the TMA bytes (or the leader's arrival); when sparse, each producer lane's own copies and, for T1, plain stores
+    for (int i = 0; i < kStages1; ++i) {
       mbar_init(smem_u32(&bars->t1_full[i]), dense ? 1 : 193);
-      mbar_init(smem_u32(&bars->t2_full[i]), dense ? 1 : 97);
       mbar_init(smem_u32(&bars->t1_empty[i]), 1);
+    }
+    for (int i = 0; i < kStages2; ++i) {
+      mbar_init(smem_u32(&bars->t2_full[i]), dense ? 1 : 97);
       mbar_init(smem_u32(&bars->t2_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars->s_full[i]), 1);
       mbar_init(smem_u32(&bars->p_full[i]), 8);
       mbar_init(smem_u32(&bars->ds_full[i]), 8);
@@ -970,7 +990,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       *reinterpret_cast<uint4*>(step_s + kStepPlane + row * 16) = make_uint4(w[4], w[5], w[6], w[7]);
     } else if (warp < 8) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
+      for (int k = 0; k < 2 * kStreamTiles; ++k)
         *reinterpret_cast<uint4*>(step_s + kStepBytes + (k * 128 + threadIdx.x - 128) * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
     fence_proxy_async_smem();

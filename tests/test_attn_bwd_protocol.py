@@ -1,9 +1,9 @@
 """Model check of the gradient kernel's barrier protocol (host only, no GPU).
 
-The kernel (svg2_attn_bwd.cu) has two kinds of unit, both with two resident tiles and two streamed ones of
-two stages each (T1: Q or K, T2: dO or V):
+The kernel (svg2_attn_bwd.cu) has two kinds of unit, both with two resident tiles and two streamed ones (T1: Q or K,
+T2: dO or V) of three stages and one:
 
-* producers fill T1(j), T2(j) into stage j % 2 and arrive on t1_full / t2_full; they wait on t1_empty / t2_empty
+* producers fill T1(j), T2(j) into stage j % stages and arrive on t1_full / t2_full; they wait on t1_empty / t2_empty
   before they reuse a stage;
 * the MMA thread issues S(j) = R1 T1(j)^T and dP(j) = R2 T2(j)^T, and the products that read P and dS from tensor
   memory in two chunks each: dV += P T2 (key unit) and dK or dQ += dS T1.  The tensor core runs them in issue order;
@@ -22,15 +22,16 @@ WARPS, PRODUCERS = 8, 3
 
 
 class Unit:
-    def __init__(self, T, key, rng, one_s_slot=False):
+    def __init__(self, T, key, rng, stages, one_s_slot=False):
         self.T, self.key, self.rng = T, key, rng
         self.slots = 1 if key or one_s_slot else 2  # S slots (one_s_slot: the planted fault of a query unit)
         two = lambda n: [Bar(n), Bar(n)]  # noqa: E731
-        self.t_full = [two(PRODUCERS), two(PRODUCERS)]
-        self.t_empty = [two(1), two(1)]
+        self.stages = stages
+        self.t_full = [[Bar(PRODUCERS) for _ in range(n)] for n in stages]
+        self.t_empty = [[Bar(1) for _ in range(n)] for n in stages]
         self.s_full, self.dp_full, self.o_full = two(1), Bar(1), Bar(1)
         self.p_full, self.ds_full = two(WARPS), two(WARPS)
-        self.smem = [[[None] * PRODUCERS for _ in range(2)] for _ in range(2)]  # [operand][stage][producer]
+        self.smem = [[[None] * PRODUCERS for _ in range(n)] for n in stages]  # [operand][stage][producer]
         self.s = [[None] * WARPS for _ in range(2)]     # what each warp finds in its part of an S slot
         self.dp = [None] * WARPS
         self.p = [[None, None] for _ in range(WARPS)]   # chunks of P and dS written
@@ -45,7 +46,8 @@ class Unit:
         elif op[0] in ("S", "dP"):
             kind, j = op
             o = 0 if kind == "S" else 1
-            check(all(x == j for x in self.smem[o][j & 1]), f"{kind}({j}) read {self.smem[o][j & 1]}")
+            at = self.smem[o][j % self.stages[o]]
+            check(all(x == j for x in at), f"{kind}({j}) read {at}")
             for w in range(WARPS):
                 if kind == "S":
                     self.s[j % self.slots][w] = j
@@ -56,7 +58,8 @@ class Unit:
         else:
             kind, j, c = op  # dV reads P and T2, the other accumulator dS and T1
             o, src = (1, self.p) if kind == "dV" else (0, self.ds)
-            check(all(x == j for x in self.smem[o][j & 1]), f"{kind}({j}) read {self.smem[o][j & 1]}")
+            at = self.smem[o][j % self.stages[o]]
+            check(all(x == j for x in at), f"{kind}({j}) read {at}")
             check(all(x[c] == j for x in src), f"{kind}({j}) chunk {c} read {src}")
             check(self.applied[kind] == 2 * j + c, f"{kind}({j}) chunk {c} out of order")
             self.applied[kind] += 1
@@ -72,10 +75,11 @@ class Unit:
     def producer(self, w):
         for j in range(self.T):
             for o in range(2):
-                if j >= 2:
-                    yield self.wait(self.t_empty[o][j & 1], (j >> 1) - 1)
-                self.smem[o][j & 1][w] = "landing"
-                self.copies.append((o, j & 1, w, j))
+                st, fill = j % self.stages[o], j // self.stages[o]
+                if fill:
+                    yield self.wait(self.t_empty[o][st], fill - 1)
+                self.smem[o][st][w] = "landing"
+                self.copies.append((o, st, w, j))
                 yield None
 
     def mma(self):
@@ -83,6 +87,7 @@ class Unit:
         commit = lambda b: q.append(("commit", b))  # noqa: E731
         if T == 0:
             return
+        S1, S2 = self.stages
         yield self.wait(self.t_full[0][0], 0)
         q.append(("S", 0))
         commit(self.s_full[0])
@@ -92,26 +97,26 @@ class Unit:
         if not key:
             commit(self.t_empty[1][0])
         for j in range(T):
-            st, nst, more = j & 1, (j + 1) & 1, j + 1 < T
+            more = j + 1 < T
             if key:
                 for c in range(2):
                     yield self.wait(self.p_full[c], j)
                     q.append(("dV", j, c))
-                commit(self.t_empty[1][st])
+                commit(self.t_empty[1][j % S2])
             if more:
-                yield self.wait(self.t_full[0][nst], (j + 1) >> 1)
+                yield self.wait(self.t_full[0][(j + 1) % S1], (j + 1) // S1)
                 q.append(("S", j + 1))
-                commit(self.s_full[0 if key else nst])
+                commit(self.s_full[0 if key else (j + 1) & 1])
             for c in range(2):
                 yield self.wait(self.ds_full[c], j)
                 q.append(("acc", j, c))
-            commit(self.t_empty[0][st])
+            commit(self.t_empty[0][j % S1])
             if more:
-                yield self.wait(self.t_full[1][nst], (j + 1) >> 1)
+                yield self.wait(self.t_full[1][(j + 1) % S2], (j + 1) // S2)
                 q.append(("dP", j + 1))
                 commit(self.dp_full)
                 if not key:
-                    commit(self.t_empty[1][nst])
+                    commit(self.t_empty[1][(j + 1) % S2])
         commit(self.o_full)
 
     def softmax(self, w):
@@ -137,9 +142,9 @@ class Unit:
             check(not self.key or self.applied["dV"] == 2 * self.T, f"epilogue saw {self.applied}")
 
 
-def run_schedule(T, key, seed, **kw):
+def run_schedule(T, key, seed, stages, **kw):
     rng = random.Random(seed)
-    k = Unit(T, key, rng, **kw)
+    k = Unit(T, key, rng, stages, **kw)
     agents = {f"producer{w}": k.producer(w) for w in range(PRODUCERS)}
     agents["mma"] = k.mma()
     agents.update({f"softmax{w}": k.softmax(w) for w in range(WARPS)})
@@ -164,11 +169,11 @@ def run_schedule(T, key, seed, **kw):
     raise ProtocolError("schedule did not finish")
 
 
-@pytest.mark.parametrize("key", [True, False], ids=["key-unit", "query-unit"])
-@pytest.mark.parametrize("T", [0, 1, 2, 3, 4, 7])
-def test_protocol_has_no_deadlock_or_hazard(T, key):
-    for seed in range(200):
-        run_schedule(T, key, seed)
+@pytest.mark.parametrize("key,stages", [(True, (3, 1)), (False, (3, 1)), (True, (2, 2)), (False, (2, 2))])
+@pytest.mark.parametrize("T", [0, 1, 2, 3, 4, 5, 9])
+def test_protocol_has_no_deadlock_or_hazard(T, key, stages):
+    for seed in range(120):
+        run_schedule(T, key, seed, stages)
 
 
 def test_the_model_sees_a_query_unit_without_its_second_s_slot():
@@ -176,7 +181,7 @@ def test_the_model_sees_a_query_unit_without_its_second_s_slot():
     hazards = 0
     for seed in range(200):
         try:
-            run_schedule(4, False, seed, one_s_slot=True)
+            run_schedule(4, False, seed, (3, 1), one_s_slot=True)
         except ProtocolError as e:
             hazards += "read S" in str(e)
     assert hazards > 0
