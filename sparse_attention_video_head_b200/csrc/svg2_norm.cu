@@ -36,7 +36,7 @@ struct NormArgs {
   T* Y;                            // Y | dX
   float* partial;                  // backward: [gridDim.x][2][W]
   float *dgamma, *dbeta;           // backward, optional
-  uint32_t* arrived;               // CTAs whose partial row is written, or null: another kernel adds the rows
+  uint32_t* arrived;               // FUSED: CTAs whose partial row is written
   long long rows;
   int W;
   int x_mis;               // X's elements past a 16-byte boundary
@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const NormArgs<T> a) {
   cp_async_wait<0>();
 }
 
-template <class T, bool EDGE, int G, int NV, int R, int STAGES, int MAXT>
+// FUSED: the CTA that comes last adds up the partial rows (a kernel of its own for that: its code cost the main loop of
+// the others 5 to 9 %).
+template <class T, bool EDGE, int G, int NV, int R, int STAGES, int MAXT, bool FUSED>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs<T> a) {
   constexpr int V = kVec<T>, P = V / 2;
   // [STAGES][R][2][NV][blockDim.x], then gamma of each thread's columns [NV][V / 4][blockDim.x]; at the end the
@@ -452,9 +454,8 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs<T> a) {
       out[c] = s;
     }
   }
-  if (a.arrived == nullptr) return;
-  // Few partial rows: the CTA that comes last adds them up, row by row in order whoever it is, and leaves the
-  // counter at zero for the next call.
+  if constexpr (!FUSED) return;
+  // row by row in order, whichever CTA it is; the counter is left at zero for the next call
   __shared__ bool last;
   __threadfence();
   __syncthreads();
@@ -501,19 +502,20 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restri
 }
 
 template <class T, bool BWD, bool EDGE, int G, int NV, int R, int STAGES, int MAXT>
-cudaError_t run_norm(NormArgs<T> a, int threads, int max_parts, int* parts, cudaStream_t s) {
+cudaError_t run_norm(const NormArgs<T>& a, int threads, int max_parts, int* parts, cudaStream_t s) {
   constexpr int V = kVec<T>;
-  constexpr auto kernel =
-      BWD ? norm_bwd_kernel<T, EDGE, G, NV, R, STAGES, MAXT> : norm_fwd_kernel<T, EDGE, G, NV, R, STAGES, MAXT>;
+  auto* kernel = BWD ? norm_bwd_kernel<T, EDGE, G, NV, R, STAGES, MAXT, false> : norm_fwd_kernel<T, EDGE, G, NV, R, STAGES, MAXT>;
   const int per_cta = G == 0 ? 1 : threads / G;
   size_t smem = static_cast<size_t>(STAGES) * R * (BWD ? 2 : 1) * NV * threads * 16;
   if (BWD) smem += static_cast<size_t>(NV) * V * threads * 4;
   if (BWD && G != 0) smem = std::max(smem, static_cast<size_t>(16) * a.W * 4);
   cudaError_t e = cudaSuccess;
+  long long grid = (a.rows + per_cta - 1) / per_cta;
+  const bool fused = BWD && grid <= kNormSms && grid * 2 * a.W <= kNormFusedValues;
+  if (fused) kernel = norm_bwd_kernel<T, EDGE, G, NV, R, STAGES, MAXT, true>;
   // (48 KB, less the static buffer, need no permission)
   if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  long long grid = (a.rows + per_cta - 1) / per_cta;
   if (grid > kNormSms) {  // as many CTAs as are resident at once
     int resident = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, smem);
@@ -524,8 +526,7 @@ cudaError_t run_norm(NormArgs<T> a, int threads, int max_parts, int* parts, cuda
   if (BWD && grid > max_parts) grid = max_parts;
   if (EDGE && G == 0 && grid < a.rows) grid = std::max(8LL, grid / 8 * 8);  // a CTA's rows are a multiple of 8 apart
   *parts = static_cast<int>(grid);
-  if (BWD && grid * 2 * a.W <= kNormFusedValues) *parts = 0;
-  else a.arrived = nullptr;
+  if (fused) *parts = 0;
   kernel<<<static_cast<unsigned>(grid), threads, smem, s>>>(a);
   return cudaGetLastError();
 }
