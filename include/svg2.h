@@ -75,8 +75,8 @@ typedef enum { SVG2_INIT_GIVEN = 0, SVG2_INIT_KMEANSPP = 1 } svg2_init;
 /* Human-readable name of a status code (static string, never NULL). */
 SVG2_API const char* svg2_status_string(int status);
 
-/* Bytes of workspace that svg2_layer needs for these sizes; every other entry point needs at
- * most this much for the same sizes.  Returns SVG2_ERR_INVALID_ARG / UNSUPPORTED on bad sizes. */
+/* Bytes of workspace that svg2_layer needs for these sizes; every other entry point without a size
+ * function of its own needs at most this much for the same sizes.  Returns SVG2_ERR_INVALID_ARG / UNSUPPORTED on bad sizes. */
 SVG2_API int svg2_workspace_size(int B, int H, int N, int d, int nQ, int nK, size_t* bytes);
 
 /* Reads and clears the device status word in `ws` after synchronising `stream`.
@@ -229,7 +229,7 @@ SVG2_API int svg2_sparse_attn_fp8(const void* Qp8, const void* Kp8, const void* 
  * reference the sparse layer is compared with at top-p = 1.
  *   Q, K, V  bf16 [B,H,N,d] (d = 128 or 64), row-major; O bf16 [B,H,N,d], out (may not alias Q, K, V).
  *   ws       at least svg2_dense_attn_workspace_size() bytes, 256-byte aligned; holds the status
- *            word (read with svg2_check_status) and the work plan.
+ *            word (read with svg2_check_status).
  * Errors: SVG2_ERR_INVALID_ARG (null or unaligned pointers, non-finite scale), SVG2_ERR_UNSUPPORTED
  * (sizes), SVG2_ERR_WORKSPACE, SVG2_ERR_CUDA (launch). */
 SVG2_API int svg2_dense_attn_workspace_size(int B, int H, int N, int d, size_t* bytes);
@@ -242,9 +242,9 @@ SVG2_API int svg2_dense_attn(const void* Q, const void* K, const void* V, int B,
  *
  * svg2_dense_attn_lse / svg2_sparse_attn_lse are svg2_dense_attn / svg2_sparse_attn (same arguments,
  * workspace, errors and O, bit for bit) that also write
- *   (scale must be finite and at least 1e-30 here and in the gradient calls: SVG2_ERR_INVALID_ARG otherwise)
  *   lse      float [B,H,N], out: lse_i = log sum_j exp(scale * q_i.k_j) over the row's keys, indexed by
- *            (permuted) row, whether perm_q is given or not; -inf for a row that keeps no key (O is 0). */
+ *            (permuted) row, whether perm_q is given or not; -inf for a row that keeps no key (O is 0).
+ * Here and in the gradient calls scale must be finite and at least 1e-30 (else SVG2_ERR_INVALID_ARG). */
 SVG2_API int svg2_dense_attn_lse(const void* Q, const void* K, const void* V, int B, int H, int N, int d, float scale,
                                  void* O, float* lse, void* ws, size_t ws_bytes, void* stream);
 SVG2_API int svg2_sparse_attn_lse(const void* Qp, const void* Kp, const void* Vp, const int32_t* q_off,
@@ -260,7 +260,8 @@ SVG2_API int svg2_sparse_attn_lse(const void* Qp, const void* Kp, const void* Vp
  *   ws              at least svg2_dense_attn_bwd_workspace_size() bytes, 256-byte aligned (enough for
  *                   svg2_dense_attn_lse too); holds the status word.
  * P and dS are rounded to bf16 for the products, sums are float32; the results are the same on every run.
- * Errors as svg2_dense_attn. */
+ * A NaN or infinity in a row reaches the gradients of the rows it shares a key or query with.  Errors as
+ * svg2_dense_attn. */
 SVG2_API int svg2_dense_attn_bwd_workspace_size(int B, int H, int N, int d, size_t* bytes);
 SVG2_API int svg2_dense_attn_bwd(const void* Q, const void* K, const void* V, const void* O, const float* lse,
                                  const void* dO, int B, int H, int N, int d, float scale, void* dQ, void* dK,
@@ -278,7 +279,8 @@ SVG2_API int svg2_dense_attn_bwd(const void* Q, const void* K, const void* V, co
  *            given, else by permuted row.  Rows that no kept pair holds get zeros; rows outside
  *            every cluster are not written.
  *   ws       at least svg2_sparse_attn_bwd_workspace_size() bytes (enough for svg2_sparse_attn_lse too).
- * Errors as svg2_sparse_attn. */
+ * Rows of neighbouring clusters may be computed together, so a NaN or infinity in Q, K, V, O, dO or lse may also
+ * reach gradients of rows whose clusters do not keep the row that holds it.  Errors as svg2_sparse_attn. */
 SVG2_API int svg2_sparse_attn_bwd_workspace_size(int B, int H, int N, int d, int nQ, int nK, size_t* bytes);
 SVG2_API int svg2_sparse_attn_bwd(const void* Qp, const void* Kp, const void* Vp, const void* O, const float* lse,
                                   const void* dO, const int32_t* q_off, const int32_t* k_off,
