@@ -45,10 +45,12 @@ constexpr int kBwdMmaWarp = 8, kBwdProducerWarp = 9;
 constexpr int kBwdMaxRanges = 1024;
 constexpr uint32_t kGatherSleep = 32;
 constexpr float kLog2e = 1.4426950408889634f;
-// Of every 16 column pairs, this many get 2^x from the cubic on the FMA pipe, the rest from the MUFU: P and dS
-// follow one another in the same warps, so the exponentials' time counts in full (2 x 50000 x 128: 7.32 ms
-// with 8, 7.57 ms with 4).
-constexpr int kBwdCubicPairs = 8;
+// Of every 16 column pairs, this many get 2^x from the cubic on the FMA pipe, the rest from the MUFU.  Dense: P and
+// dS follow one another in the same warps, so the exponentials' time counts in full (2 x 75600 x 128: 15.0 ms with 8
+// in both kinds of unit, 15.3 to 15.6 with 4 or 10 in one of them).  Sparse: the three gathering warps issue from the same
+// schedulers, and the cubic's instructions cost more than the MUFU saves (2 x 75600 x 128: 6.12 ms with 0, 6.22 with
+// 2, 6.26 with 4, 6.45 with 6, 6.59 with 8; 8 x 12480 in 64 / 256 clusters: 1.88 against 2.03 ms with 8).
+constexpr int kBwdCubicDense = 8, kBwdCubicSparse = 0;
 
 template <int D>
 constexpr uint32_t bwd_tile_bytes() { return 128u * D * 2u; }
@@ -716,7 +718,8 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
           for (int e = 16 * c; e < 16 * c + 16; ++e) {
             const float2 x = make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1]));
             const float2 t = KV ? mul2(x, scl) : fma2(x, scl, make_float2(nl_row, nl_row));
-            p[e] = ((e & 15) >= 16 - kBwdCubicPairs) ? exp2_cubic2(t) : make_float2(fast_exp2(t.x), fast_exp2(t.y));
+            p[e] = ((e & 15) >= 16 - (DENSE ? kBwdCubicDense : kBwdCubicSparse)) ? exp2_cubic2(t)
+                                                                                   : make_float2(fast_exp2(t.x), fast_exp2(t.y));
           }
           if constexpr (KV) {
             uint32_t pk[16];
@@ -936,6 +939,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   BwdUnit un;
   if (dense) un = BwdUnit{0, u * 128, min(128, a.N - u * 128), 1};
   else un = (kv ? a.k_units : a.q_units)[idx];
+  if constexpr (!dense) {  // (malformed offsets can make two runs of the plan write one slot)
+    un.nrows = min(un.nrows, a.N - un.row0);
+    un.nseg = min(un.nseg, (kv ? a.nK : a.nQ) - un.cluster);
+  }
   if (un.nrows <= 0) return;
   const long long wb = effective_wait_budget(a.wait_budget);
 

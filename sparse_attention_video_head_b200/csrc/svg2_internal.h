@@ -208,7 +208,7 @@ struct BwdUnit {
   int32_t cluster;  // the first row's
   int32_t row0;     // first permuted row
   int32_t nrows;    // 1..128; 0: no unit
-  int32_t nseg;     // clusters from the first row's to the last row's (empty ones counted), at most 16
+  int32_t nseg;     // clusters from the first row's to the last row's (empty ones counted), at most 12
 };
 
 inline int bwd_max_units_per_head(int N, int n) { return N / 128 + n; }
