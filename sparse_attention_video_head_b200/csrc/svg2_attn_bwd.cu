@@ -105,6 +105,11 @@ __device__ __forceinline__ uint4 three_bf16(float v) {
 // hold like keys, and there the products are not what takes the time: over random short rows (2 to 512 keys)
 // the worst error of dQ and dK falls from 5.8e-3 and 3.0e-2 to 4.9e-3 and 2.1e-3 of their norms.
 constexpr int kBwdSplitTiles = 4;
+// Query units with streams up to this long do so for the second chunk of every tile (template SPLIT = 1; 2: both
+// chunks): dQ is then 2.1 to 2.2e-3 of its norm off instead of 2.45 to 2.6e-3 (1.66e-3 is its own rounding), for 0 to 2 %
+// of the gradients' time on 6 x 1333 x 64 and 1 x 4096 x 64 sparse, 7 to 14 % on 24 x 4096 x 64 and 8 x 2500 x 128.  Longer
+// streams, where the products are all of the time, stay at 2.4 to 2.5e-3.
+constexpr int kBwdHalfSplitTiles = 32;
 
 struct BwdMaps {  // Q, K, V, dO by [plane, row, column]: boxes of 128 rows x 64 columns, 128-byte swizzle
   CUtensorMap m[4];
@@ -392,7 +397,7 @@ struct BwdTmem {
   static constexpr uint32_t dp = 256, acc2 = 384;     // acc2: dK | dQ
 };
 
-template <int D, bool DENSE, bool KV, bool SPLIT, bool MULTI>
+template <int D, bool DENSE, bool KV, int SPLIT, bool MULTI>
 __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, const BwdUnit un, const int bh,
                                          uint8_t* smem, BwdBars* bars, float* stats, const int32_t* r_start,
                                          const int32_t* r_cum, const uint16_t* r_seg, uint8_t* step_s, float* scratch, const long long wb) {
@@ -489,7 +494,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
           if (!ok) break;
           tc_fence_after();
           accumulate(tmem + Tm::acc2, tmem + Tm::dp, t1 + c1 * kTile, c, j > 0 || c > 0);  // dK += dS^T Q | dQ += dS K
-          if constexpr (SPLIT) accumulate(tmem + Tm::acc2, tmem + Tm::dp + 32, t1 + c1 * kTile, c, true);
+          if (SPLIT > 1 - c) accumulate(tmem + Tm::acc2, tmem + Tm::dp + 32, t1 + c1 * kTile, c, true);
         }
         if (!ok) break;
         mma_commit(smem_u32(&bars->t1_empty[c1]));
@@ -681,7 +686,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
     auto wait = [&](uint64_t* bar, int phase) {
       return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), phase & 1, st, kWhereAttnBwdSoftmax, wb));
     };
-    const bool exact_delta = SPLIT && T == 1 && (!KV || (DENSE && a.N <= 128));
+    const bool exact_delta = SPLIT == 2 && T == 1 && (!KV || (DENSE && a.N <= 128));
     auto all_softmax_warps = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     auto hand_over = [&](uint64_t* bar) {
       tmem_wait_st();
@@ -742,7 +747,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       tmem_ld32p(t_dp, sv);
       tmem_wait_ld();
       tmem_ld32p(t_dp + 32, sv + 32);
-      if constexpr (SPLIT) tmem_wait_ld();  // (the second halves of dS go where dP's second chunk is)
+      if constexpr (SPLIT == 2) tmem_wait_ld();  // (the second halves of dS go where dP's second chunk is)
       if (exact_delta) {
         // delta_i = sum_j P_ij dP_ij in float32 (key unit: what is missing in dP' = dP - delta)
         if constexpr (KV) {  // over the lanes and the four warps: this CTA holds every key of the plane
@@ -786,26 +791,27 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (c == 1) tmem_wait_ld();
-        uint32_t hi[16], lo[SPLIT ? 16 : 1];
+        uint32_t hi[16], lo[SPLIT != 0 ? 16 : 1];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int k = 16 * c + e;
           float2 x = make_float2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1]));
           if constexpr (!KV) x = add2(x, make_float2(nd_row, nd_row));
-          else if constexpr (SPLIT)
+          else if constexpr (SPLIT == 2)
             if (exact_delta) x = add2(x, *reinterpret_cast<const float2*>(stats + 128 + half * 64 + 2 * k));
           const float2 ds = mul2(p[k], x);
           hi[e] = pack_bf16x2(ds.x, ds.y);
-          if constexpr (SPLIT) lo[e] = pack_bf16x2(ds.x - bf16lo_to_f32(hi[e]), ds.y - bf16hi_to_f32(hi[e]));
+          if (SPLIT > 1 - c) lo[SPLIT != 0 ? e : 0] = pack_bf16x2(ds.x - bf16lo_to_f32(hi[e]), ds.y - bf16hi_to_f32(hi[e]));
         }
         tmem_st16(t_dp + 16 * c, hi);
-        if constexpr (SPLIT) tmem_st16(t_dp + 32 + 16 * c, lo);
+        if constexpr (SPLIT != 0)
+          if (SPLIT > 1 - c) tmem_st16(t_dp + 32 + 16 * c, lo);
         hand_over(&bars->ds_full[c]);
         if constexpr (!KV) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             r_sum = add2(r_sum, make_float2(bf16lo_to_f32(hi[e]), bf16hi_to_f32(hi[e])));
-            if constexpr (SPLIT) r_sum = add2(r_sum, make_float2(bf16lo_to_f32(lo[e]), bf16hi_to_f32(lo[e])));
+            if (SPLIT > 1 - c) r_sum = add2(r_sum, make_float2(bf16lo_to_f32(lo[SPLIT != 0 ? e : 0]), bf16hi_to_f32(lo[SPLIT != 0 ? e : 0])));
           }
         }
       }
@@ -923,7 +929,7 @@ __device__ __forceinline__ void build_ranges(const BwdArgs& a, const BwdUnit un,
 
 // Dense attention with long and with short streams, and the sparse plan, are kernels of their own: each holds
 // only the unit variants that it can meet, which keeps the hot loops' registers free of spills.
-enum class BwdKind { kDense, kDenseShort, kSparse };
+enum class BwdKind { kDense, kDenseMid, kDenseShort, kSparse };
 
 template <int D, BwdKind KIND>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -1015,19 +1021,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #define SVG2_BWD_UNIT(KV, SPLIT, MULTI) \
   bwd_unit<D, dense, KV, SPLIT, MULTI>(maps, a, un, bh, smem, bars, stats, r_start, r_cum, r_seg, step_s, scratch, wb)
   if constexpr (dense) {
-    constexpr bool kShort = KIND == BwdKind::kDenseShort;
-    if (kv) SVG2_BWD_UNIT(true, kShort, false);
-    else SVG2_BWD_UNIT(false, kShort, false);
+    constexpr int kSplitQ = KIND == BwdKind::kDenseShort ? 2 : (KIND == BwdKind::kDenseMid ? 1 : 0);
+    if (kv) SVG2_BWD_UNIT(true, KIND == BwdKind::kDenseShort ? 2 : 0, false);
+    else SVG2_BWD_UNIT(false, kSplitQ, false);
   } else {
     const bool split = bars->L <= kBwdSplitTiles * 128, multi = un.nseg > 1;
     if (kv) {
-      if (split) SVG2_BWD_UNIT(true, true, true);  // (with one cluster its mask drops nothing)
-      else if (multi) SVG2_BWD_UNIT(true, false, true);
-      else SVG2_BWD_UNIT(true, false, false);
+      if (split) SVG2_BWD_UNIT(true, 2, true);  // (with one cluster its mask drops nothing)
+      else if (multi) SVG2_BWD_UNIT(true, 0, true);
+      else SVG2_BWD_UNIT(true, 0, false);
     } else {
-      if (split) SVG2_BWD_UNIT(false, true, true);
-      else if (multi) SVG2_BWD_UNIT(false, false, true);
-      else SVG2_BWD_UNIT(false, false, false);
+      if (split) SVG2_BWD_UNIT(false, 2, true);
+      else if (bars->L <= kBwdHalfSplitTiles * 128) SVG2_BWD_UNIT(false, 1, true);
+      else if (multi) SVG2_BWD_UNIT(false, 0, true);
+      else SVG2_BWD_UNIT(false, 0, false);
     }
   }
 #undef SVG2_BWD_UNIT
@@ -1102,8 +1109,9 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   a.dO = static_cast<const __nv_bfloat16*>(base[3]);
   if (e != cudaSuccess) return e;
   auto* kernel = !dense ? attn_bwd_kernel<D, BwdKind::kSparse>
-                        : (N <= kBwdSplitTiles * 128 ? attn_bwd_kernel<D, BwdKind::kDenseShort>
-                                                     : attn_bwd_kernel<D, BwdKind::kDense>);
+                 : N <= kBwdSplitTiles * 128  ? attn_bwd_kernel<D, BwdKind::kDenseShort>
+                 : N <= kBwdHalfSplitTiles * 128 ? attn_bwd_kernel<D, BwdKind::kDenseMid>
+                                              : attn_bwd_kernel<D, BwdKind::kDense>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bwd_smem<D>());
   if (e != cudaSuccess) return e;
   const long long units = static_cast<long long>(BH) * (a.k_per_head + a.q_per_head);

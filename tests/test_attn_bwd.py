@@ -473,3 +473,98 @@ def test_training_layer(sparse):
         layer.forward(Q, K, V, **params, init=svg2.SVG2_INIT_GIVEN)
         layer.backward(dO)
         svg2.raise_on_device_error(layer.ws)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sparse", [False, True])
+def test_offsets_past_32_bits(sparse):
+    """18000 planes of 1000 x 128: 2.3e9 elements per tensor.  They repeat three planes, so every result does."""
+    svg2 = require_gpu()
+    g = gen(21)
+    N, d, times = 1000, 128, 6000
+    base = [randn(g, 1, 3, N, d) for _ in range(4)]
+    big = [x.repeat(1, times, 1, 1) for x in base]
+    assert big[0].numel() > 2 ** 31
+    if sparse:
+        pl = plan(22, 1, 3, N, 6, 9, 0.5)
+        ref = sparse_step(svg2, pl, *base, 0.1)
+        many = {n: x.repeat(1, times, *[1] * (x.dim() - 2)) if torch.is_tensor(x) and x.dim() > 2 else x for n, x in pl.items()}
+        got = sparse_step(svg2, many, *big, 0.1)
+    else:
+        ref = dense_step(svg2, *base, 0.1)
+        got = dense_step(svg2, *big, 0.1)
+    del big
+    for n in ref:
+        parts = got[n].view(times, 3, *ref[n].shape[2:])
+        for i in range(0, times, 500):
+            assert (parts[i:i + 500] == ref[n]).all(), (n, i)
+
+
+@pytest.mark.gpu
+def test_as_many_planes_as_allowed():
+    """65535 planes of one token: P = 1 within EP, so O = V, dV = dO within EP and a rounding, and dS = P dP (1 - P)."""
+    svg2 = require_gpu()
+    g = gen(23)
+    Q, K, V, dO = (randn(g, 5, 13107, 1, 64) for _ in range(4))
+    got = {n: x.double() for n, x in dense_step(svg2, Q, K, V, dO, 0.125).items()}
+    q, k, v, do = (x.double() for x in (Q, K, V, dO))
+    es = 66 * 2.0 ** -24 * 0.125 * (q * k).abs().sum(3, keepdim=True)
+    ep = (2 * 7.5e-5 + 2 * es) * 1.01
+    assert ((got["O"] - v).abs() <= (ep + U) * 1.02 * v.abs()).all()
+    assert ((got["dV"] - do).abs() <= (ep + U) * 1.02 * do.abs()).all()
+    assert ((got["lse"] - 0.125 * (q * k).sum(3)).abs() <= (7.5e-5 + 2 * es[..., 0]) * 1.02 + 2.0 ** -22 * got["lse"].abs()).all()
+    ds = ep * (do * v).abs().sum(3, keepdim=True) * (1 + 2 * U)
+    assert (got["dK"].abs() <= 0.125 * ds * q.abs() * 1.02).all()
+    assert (got["dQ"].abs() <= 0.125 * ds * 2 * k.abs() * 1.02).all()  # dS k - (its sum) times the mean key
+
+
+@pytest.mark.gpu
+def test_debug_build_of_the_gradients():
+    """The library with its bounds checks: nothing is reported on good plans; offsets that do not ascend or
+    reach past the plane, and a permutation entry out of range, are."""
+    from sparse_attention_video_head_b200 import build
+    svg2 = require_gpu()
+    g = gen(24)
+    B, H, N, d, nQ, nK = 1, 2, 1500, 64, 40, 70
+    Q, K, V, dO = (randn(g, B, H, N, d) for _ in range(4))
+    pl = plan(25, B, H, N, nQ, nK, 0.5)
+    ref = sparse_step(svg2, pl, Q, K, V, dO, 0.125)
+    dref = dense_step(svg2, Q, K, V, dO, 0.125)
+    build.build(debug=True)
+    svg2.use_debug_library(True)
+    try:
+        got, dgot = sparse_step(svg2, pl, Q, K, V, dO, 0.125), dense_step(svg2, Q, K, V, dO, 0.125)
+        for n in ref:
+            assert torch.equal(got[n], ref[n]) and torch.equal(dgot[n], dref[n]), n
+        ws = svg2.sparse_bwd_workspace(B, H, N, d, nQ, nK)
+        for name, at, value in (("k_off", 3, N + 5), ("q_off", 20, -7), ("k_off", 40, 0), ("perm_q", 11, N), ("perm_k", 12, -1)):
+            bad = {n: x.clone() if torch.is_tensor(x) else x for n, x in pl.items()}
+            bad[name][0, 1, at] = value
+            grads = [torch.zeros_like(Q) for _ in range(3)]
+            svg2.svg2_sparse_attn_bwd(Q, K, V, ref["O"], ref["lse"], dO, *(bad[n] for n in ("q_off", "k_off", "sel_count", "sel_idx")),
+                                      0.125, *grads, ws, perm_q=bad["perm_q"], perm_k=bad["perm_k"])
+            with pytest.raises(svg2.Svg2Error) as e:
+                svg2.raise_on_device_error(ws)
+            assert e.value.code == 6, name
+    finally:
+        svg2.use_debug_library(False)
+
+
+@pytest.mark.gpu
+def test_malformed_offsets_stay_in_their_planes():
+    """Offsets of one plane that do not ascend: the other plane's gradients are what they were."""
+    svg2 = require_gpu()
+    g = gen(26)
+    B, H, N, d, nQ, nK = 1, 2, 1500, 64, 70, 90
+    Q, K, V, dO = (randn(g, B, H, N, d) for _ in range(4))
+    pl = plan(27, B, H, N, nQ, nK, 0.5)
+    ref = sparse_step(svg2, pl, Q, K, V, dO, 0.125, perms=False)
+    for name, n in (("q_off", nQ), ("k_off", nK)):
+        pl[name][0, 1] = torch.randint(-50, N + 50, (n + 1,), device="cuda", generator=g, dtype=torch.int32)
+    ws = svg2.sparse_bwd_workspace(B, H, N, d, nQ, nK)
+    grads = [torch.full_like(Q, 3.0) for _ in range(3)]
+    svg2.svg2_sparse_attn_bwd(Q, K, V, ref["O"], ref["lse"], dO, *(pl[n] for n in ("q_off", "k_off", "sel_count", "sel_idx")),
+                              0.125, *grads, ws)
+    svg2.raise_on_device_error(ws)
+    for n, x in zip(("dQ", "dK", "dV"), grads):
+        assert torch.equal(x[0, 0], ref[n][0, 0]), n

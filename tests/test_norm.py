@@ -178,3 +178,54 @@ def test_gradients_against_differences():
             flat[i] = keep
             # differences: h^2 times a third derivative of order 1, and 1e-15 / h of rounding
             assert abs((up - down).item() / (2 * h) - got.flatten()[i].item()) <= 1e-6
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """17 million rows of 128: 2.2e9 elements, a block of 1000 rows repeated, so its results are too."""
+    svg2 = require_gpu()
+    X, dY, gamma, beta = make(31, 1000, 128, torch.bfloat16)
+    ref = both(svg2, X, dY, gamma, beta)
+    times = 17000
+    got = both(svg2, X.repeat(times, 1), dY.repeat(times, 1), gamma, beta)
+    assert got[0].numel() > 2 ** 31
+    for i in range(4):  # Y, mean, rstd, dX
+        parts = got[i].view(times, *ref[i].shape)
+        for t in range(0, times, 1000):
+            assert (parts[t:t + 1000] == ref[i]).all(), (i, t)
+
+
+@pytest.mark.gpu
+def test_one_workspace_for_calls_of_all_kinds():
+    """Few rows (the last CTA adds the partial rows) and many (another kernel does), in turn, and replayed."""
+    svg2 = require_gpu()
+    sizes = [(300, 64), (40000, 64), (37, 77), (5, 8192), (2000, 1000), (1, 8)]
+    ws = svg2.layer_norm_bwd_workspace(40000, 8192)
+    calls = []
+    for i, (rows, width) in enumerate(sizes):
+        X, dY, gamma, beta = make(40 + i, rows, width, torch.bfloat16)
+        _, mean, rstd, dX, dgamma, dbeta = both(svg2, X, dY, gamma, beta)
+        out = [torch.empty_like(t) for t in (dX, dgamma, dbeta)]
+        calls.append((lambda X=X, dY=dY, gamma=gamma, mean=mean, rstd=rstd, out=out:
+                      svg2.svg2_layer_norm_bwd(X, dY, gamma, mean, rstd, *out, ws), out, (dX, dgamma, dbeta)))
+    def compare():
+        torch.cuda.synchronize()
+        for (_, out, ref), size in zip(calls, sizes):
+            assert all(torch.equal(a, b) for a, b in zip(out, ref)), size
+            for t in out:
+                t.fill_(torch.nan)
+    for _ in range(2):
+        for call, _, _ in calls:
+            call()
+        compare()
+    graphs = []
+    for part in (calls[:3], calls[3:]):  # two graphs share the workspace, one after the other
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for call, _, _ in part:
+                call()
+        graphs.append(graph)
+    for _ in range(3):
+        for graph in graphs:
+            graph.replay()
+        compare()
