@@ -99,8 +99,8 @@ __device__ __forceinline__ uint4 three_bf16(float v) {
   return make_uint4(finite ? hi | (mid << 16) : hi, finite ? lo : 0u, 0u, 0u);
 }
 
-// Streams of up to this many tiles hand dS over as two bf16 numbers (its rounding, and the rest) and take one
-// more product per tile; one-tile streams also take delta as sum_j P_ij dP_ij instead of from the bf16 O
+// Streams of up to this many tiles hand P and dS over as two bf16 numbers each (the rounding, and the rest) and take a
+// product more for each; one-tile streams also take delta as sum_j P_ij dP_ij instead of from the bf16 O
 // (the key unit only when it holds every key, dense N <= 128).  Short rows average fewer rounding errors and often
 // hold like keys, and there the products are not what takes the time: over random short rows (2 to 512 keys)
 // the worst error of dQ and dK falls from 5.8e-3 and 3.0e-2 to 4.9e-3 and 2.1e-3 of their norms.
@@ -254,17 +254,22 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
 // A unit costs as many tiles as its stream is long, however few of its 128 rows are used, and clusters
 // rarely end on a multiple of 128.  So what is left of a cluster after its full tiles shares a unit with the
 // rows that follow; the joint stream is the union of the clusters' streams, and the pairs that a row's own
-// cluster does not keep are masked.  On 8 heads of 12480 tokens in 64 / 256 clusters (49 rows per K cluster),
-// 60 % kept, the gradients took 2.91 ms with units of one cluster each and take 1.81 ms.
+// cluster does not keep are masked.
 // ------------------------------------------------------------------------------------------------
 
 // One warp packs clusters [c0, c1) into units, lane w holding word w of the clusters' bits; lane 0 calls
 // emit(i, unit) in order.
 //
-// A unit takes t rows of the next cluster if that leaves the cluster a unit less (a union is never longer than
-// its parts), or if the stream grows by less than half of what t of a unit's 128 rows cost: the room serves
-// the rows to come.  (Half: over the plans of the tests and the 720p layer the sum of the streams came out
-// within 3 % of the best of 0, 0.5, 0.7, 1 and always, each of which loses 5 to 35 % on some.)
+// A unit takes t rows of the next cluster where that shortens the streams, in words of the clusters' bits.  It adds what
+// the cluster's stream has beyond the unit's, and a quarter (kMaskCost / 16) of the joint stream where the unit is
+// the first time of several clusters, of the addition later: the masking, and a last wave with fewer and longer units.
+// It saves a unit of the cluster's own stream if the cluster needs one less (the room that is left counts a third of
+// that, for the rows to come); if not, half of what t of a unit's 128 rows cost.  Gradients in us with a cost of 0, 2, 4, 6
+// sixteenths: 2 x 75600 in 100 / 500 clusters, 28 % kept, 6784, 6379, 5803, 6026 (5884 without sharing); 8 x 12480 in 64 / 256,
+// 60 %: 2016, 1886, 1883, 2057 (2330); 3 x 20000 in 300 / 300, 30 %: 1432, 1429, 1173, 1146 (1154); with the room counted, 4 x
+// 16000 in 400 / 64, 40 %: 1344 -> 1201.
+constexpr int kMaskCost = 4;
+
 template <class Emit>
 __device__ __forceinline__ void pack_units(const int32_t* off, const uint32_t* bits, int W, int c0, int c1, int N,
                                           Emit&& emit) {
@@ -283,7 +288,11 @@ __device__ __forceinline__ void pack_units(const int32_t* off, const uint32_t* b
       const int t = min(128 - rows, left);
       const int added = __reduce_add_sync(0xffffffffu, __popc(mine & ~joint));
       const int all = __reduce_add_sync(0xffffffffu, __popc(mine | joint));
-      if (((left - t + 127) >> 7) < ((left + 127) >> 7) || added * 256 < t * all) {
+      const int mask = kMaskCost * (last > first ? added : all);
+      const int own = __reduce_add_sync(0xffffffffu, __popc(mine));
+      const int gain = ((left - t + 127) >> 7) < ((left + 127) >> 7) ? 16 * own + own * (128 - rows - t) / 24
+                                                                           : t * all / 16;
+      if (16 * added + mask < gain) {
         rows += t;
         last = j;
         joint |= mine;
@@ -474,6 +483,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
             if (!ok) break;
             tc_fence_after();
             accumulate(tmem + Tm::acc1, tmem, t2 + c2 * kTile, c, j > 0 || c > 0);  // dV += P^T dO
+            if constexpr (SPLIT == 2) accumulate(tmem + Tm::acc1, tmem + 32, t2 + c2 * kTile, c, true);
           }
           if (!ok) break;
           mma_commit(smem_u32(&bars->t2_empty[c2]));
@@ -709,6 +719,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         tmem_ld32p(t_s, sv);
         tmem_wait_ld();
         tmem_ld32p(t_s + 32, sv + 32);
+        if constexpr (KV && SPLIT == 2) tmem_wait_ld();  // (the rests of P's first chunk go where S's second chunk is)
         const int valid = L - j * 128 - half * 64;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -731,6 +742,12 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(p[16 * c + e].x, p[16 * c + e].y);
             tmem_st16(t_s + 16 * c, pk);
+            if constexpr (SPLIT == 2) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                pk[e] = pack_bf16x2(p[16 * c + e].x - bf16lo_to_f32(pk[e]), p[16 * c + e].y - bf16hi_to_f32(pk[e]));
+              tmem_st16(t_s + 32 + 16 * c, pk);
+            }
             hand_over(&bars->p_full[c]);
           }
         }
