@@ -476,6 +476,195 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormArgs<T> a) {
   if (threadIdx.x == 0) *a.arrived = 0u;
 }
 
+// Rows of odd widths, many and short.  kVec rows of W elements are W whole 16-byte vectors wherever the tensor starts on
+// one, so a warp copies that many rows at a time into its own shared memory, two stages, works on them there by
+// single elements (lane l has columns l, l + 32, ...) and writes the results back over them, and to memory as whole vectors.
+// Bound by its instructions for bf16 (0.35 to 0.63 of the copy bandwidth forward, 0.42 to 0.75 backward) and by memory for
+// float32 (0.62 to 0.91).  In us, forward / backward, against the kernels above: bf16 2000000 x 77 237 / 302 (356 / 374), 1626016 x
+// 123 239 / 294 (546 / 580), 391389 x 511 196 / 362 (432 / 636); float32 784313 x 255 294 / 428 (503 / 1049).
+template <class T, int K, bool BWD>
+__global__ void __launch_bounds__(128) norm_odd_kernel(const NormArgs<T> a) {
+  constexpr int V = kVec<T>, NB = BWD ? 2 : 1, RU = K <= 4 ? 4 : (K <= 8 || !BWD ? 2 : 1);  // RU rows at a time
+  extern __shared__ uint4 ring[];  // [warps][2 stages][X, dY][W]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, W = a.W;
+  uint4* mine = ring + static_cast<size_t>(warp) * 2 * NB * W;
+  const long long tiles = (a.rows + V - 1) / V, step = static_cast<long long>(gridDim.x) * warps;
+  const float inv_w = 1.f / static_cast<float>(W);
+  auto fetch = [&](long long tile, int stage) {
+    if (tile < tiles) {
+      const long long e0 = tile * V * W;
+      uint4* to = mine + stage * NB * W;
+      if (tile * V + V <= a.rows) {
+        for (int v = lane; v < W; v += 32) {
+          cp_async16_zfill(smem_u32(to + v), a.X + e0 + v * V, true);
+          if (BWD) cp_async16_zfill(smem_u32(to + W + v), a.dY + e0 + v * V, true);
+        }
+      } else {  // the last rows: fewer than V
+        const int n = static_cast<int>(a.rows - tile * V) * W;
+        for (int e = lane; e < n; e += 32) {
+          reinterpret_cast<T*>(to)[e] = a.X[e0 + e];
+          if (BWD) reinterpret_cast<T*>(to + W)[e] = a.dY[e0 + e];
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  auto load = [](T v) { return static_cast<float>(v); };
+  long long tile = static_cast<long long>(blockIdx.x) * warps + warp;
+  fetch(tile, 0);
+  float ga[K], be[K], dg[BWD ? K : 1], db[BWD ? K : 1];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = lane + 32 * k;
+    ga[k] = a.gamma != nullptr && c < W ? __ldg(a.gamma + c) : 1.f;
+    be[k] = !BWD && a.beta != nullptr && c < W ? __ldg(a.beta + c) : 0.f;
+    if (BWD) dg[BWD ? k : 0] = db[BWD ? k : 0] = 0.f;
+  }
+  // backward: lane r holds mean and rstd of row r of the next tile
+  float mean_n = 0.f, rstd_n = 0.f;
+  auto stats = [&](long long t) {
+    const long long row = t * V + lane;
+    const bool has = lane < V && row < a.rows;
+    mean_n = has ? __ldg(a.mean_in + row) : 0.f;
+    rstd_n = has ? __ldg(a.rstd_in + row) : 0.f;
+  };
+  if (BWD) stats(tile);
+  int stage = 0, turn = 0;
+  for (; tile < tiles; tile += step) {
+    fetch(tile + step, stage ^ 1);
+    const float mean_t = mean_n, rstd_t = rstd_n;
+    if (BWD) stats(tile + step);
+    cp_async_wait<1>();
+    __syncwarp();
+    uint4* vec = mine + stage * NB * W;
+    T* xs = reinterpret_cast<T*>(vec);
+    const T* gs = reinterpret_cast<const T*>(vec + W);
+    const int rows = static_cast<int>(min(static_cast<long long>(V), a.rows - tile * V));
+    for (int r = 0; r < rows; r += RU) {
+      float x[RU][K], s[BWD ? 2 * RU : RU];
+      if constexpr (!BWD) {
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+          s[u] = 0.f;
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            x[u][k] = r + u < rows && lane + 32 * k < W ? load(xs[(r + u) * W + lane + 32 * k]) : 0.f;
+            s[u] += x[u][k];
+          }
+        }
+        group_sum<32, RU>(s, nullptr, turn);
+        float mean[RU];
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+          mean[u] = s[u] * inv_w;
+          s[u] = 0.f;
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            x[u][k] = lane + 32 * k < W ? x[u][k] - mean[u] : 0.f;
+            s[u] = fmaf(x[u][k], x[u][k], s[u]);
+          }
+        }
+        group_sum<32, RU>(s, nullptr, turn);
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+          if (r + u >= rows) continue;
+          const float rstd = rsqrtf(fmaf(s[u], inv_w, a.eps));
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+            if (lane + 32 * k < W) store_one(xs + (r + u) * W + lane + 32 * k, fmaf(x[u][k] * rstd, ga[k], be[k]));
+          if (lane == 0) {
+            if (a.mean != nullptr) a.mean[tile * V + r + u] = mean[u];
+            if (a.rstd != nullptr) a.rstd[tile * V + r + u] = rstd;
+          }
+        }
+      } else {
+        float g[RU][K], rs[RU];
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+          const float m = __shfl_sync(0xffffffffu, mean_t, (r + u) & (V - 1));
+          rs[u] = __shfl_sync(0xffffffffu, rstd_t, (r + u) & (V - 1));
+          s[2 * u] = s[2 * u + 1] = 0.f;
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            const bool in = r + u < rows && lane + 32 * k < W;
+            const int e = (r + u) * W + lane + 32 * k;
+            x[u][k] = in ? (load(xs[e]) - m) * rs[u] : 0.f;
+            const float dy = in ? load(gs[e]) : 0.f;
+            dg[k] = fmaf(dy, x[u][k], dg[k]);
+            db[k] += dy;
+            g[u][k] = dy * ga[k];
+            s[2 * u] += g[u][k];
+            s[2 * u + 1] = fmaf(g[u][k], x[u][k], s[2 * u + 1]);
+          }
+        }
+        group_sum<32, 2 * RU>(s, nullptr, turn);
+#pragma unroll
+        for (int u = 0; u < RU; ++u) {
+          if (r + u >= rows) continue;
+          const float c1 = -s[2 * u] * inv_w, c2 = -s[2 * u + 1] * inv_w;
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+            if (lane + 32 * k < W) store_one(xs + (r + u) * W + lane + 32 * k, rs[u] * fmaf(x[u][k], c2, g[u][k] + c1));
+        }
+      }
+    }
+    __syncwarp();
+    T* out = a.Y + tile * V * W;
+    if (rows == V) {
+      for (int v = lane; v < W; v += 32) reinterpret_cast<uint4*>(out)[v] = vec[v];
+    } else {
+      for (int e = lane; e < rows * W; e += 32) out[e] = xs[e];
+    }
+    __syncwarp();  // (the next copies into this stage come after every lane's reads)
+    stage ^= 1;
+  }
+  cp_async_wait<0>();
+  if constexpr (BWD) {  // the warps' column sums, added in order
+    float* cols = reinterpret_cast<float*>(ring);  // [warps][2][W]
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (lane + 32 * k < W) {
+        cols[(warp * 2 + 0) * W + lane + 32 * k] = dg[k];
+        cols[(warp * 2 + 1) * W + lane + 32 * k] = db[k];
+      }
+    __syncthreads();
+    float* out = a.partial + static_cast<size_t>(blockIdx.x) * 2 * W;
+    for (int c = threadIdx.x; c < 2 * W; c += blockDim.x) {
+      float s = 0.f;
+      for (int w = 0; w < warps; ++w) s += cols[w * 2 * W + c];
+      out[c] = s;
+    }
+  }
+}
+
+// Below, a warp's lanes are mostly idle (bf16 2000000 x 37: 208 us against 178; float32 x 21: 197 against 96); above, two
+// stages of so many rows leave few warps resident.
+constexpr int kNormOddFrom = 65, kNormOddTo = 512;
+
+template <class T, bool BWD>
+cudaError_t run_norm_odd(const NormArgs<T>& a, int max_parts, int* parts, cudaStream_t s) {
+  auto* kernel = a.W <= 96    ? norm_odd_kernel<T, 3, BWD>
+                 : a.W <= 128 ? norm_odd_kernel<T, 4, BWD>
+                 : a.W <= 192 ? norm_odd_kernel<T, 6, BWD>
+                 : a.W <= 256 ? norm_odd_kernel<T, 8, BWD>
+                 : a.W <= 384 ? norm_odd_kernel<T, 12, BWD>
+                              : norm_odd_kernel<T, 16, BWD>;
+  const int warps = a.W <= 256 ? 4 : 2;
+  const int smem = warps * 2 * (BWD ? 2 : 1) * a.W * 16;
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  int resident = 0;
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, 32 * warps, smem);
+  if (e != cudaSuccess) return e;
+  const long long tiles = (a.rows + kVec<T> - 1) / kVec<T>;
+  long long grid = std::min((tiles + warps - 1) / warps, static_cast<long long>(kNormSms) * std::max(1, resident));
+  if (BWD) grid = std::min(grid, static_cast<long long>(max_parts));
+  *parts = static_cast<int>(grid);
+  kernel<<<static_cast<unsigned>(grid), 32 * warps, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 // dgamma, dbeta = the column sums of the partial rows, 32 columns per CTA: warp w adds rows w, w + 32, ...,
 // then the warps' sums are added in order.
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* __restrict__ partial, int parts, int W,
@@ -582,7 +771,11 @@ cudaError_t run_typed(const NormCall& n, bool bwd, cudaStream_t s) {
   int parts = 0;
   const int max_parts = norm_max_parts(n.rows);
   const bool edge = a.W % kVec<T> != 0 || a.x_mis != 0 || !a.y_same || (bwd && !a.dy_same);
-  cudaError_t e = bwd ? (edge ? pick_norm<T, true, true>(a, max_parts, &parts, s)
+  // many odd rows that start together on 16 bytes
+  const bool odd = edge && a.x_mis == 0 && a.y_same && (!bwd || a.dy_same) && a.W >= kNormOddFrom && a.W <= kNormOddTo &&
+                   a.rows >= 4LL * kNormSms * kVec<T>;
+  cudaError_t e = odd ? (bwd ? run_norm_odd<T, true>(a, max_parts, &parts, s) : run_norm_odd<T, false>(a, max_parts, &parts, s))
+                  : bwd ? (edge ? pick_norm<T, true, true>(a, max_parts, &parts, s)
                               : pick_norm<T, true, false>(a, max_parts, &parts, s))
                       : (edge ? pick_norm<T, false, true>(a, max_parts, &parts, s)
                               : pick_norm<T, false, false>(a, max_parts, &parts, s));

@@ -229,3 +229,30 @@ def test_one_workspace_for_calls_of_all_kinds():
         for graph in graphs:
             graph.replay()
         compare()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,width,affine", [
+    (4736, 1, True), (4739, 3, True), (5001, 31, False), (4999, 33, True), (6007, 77, True), (5003, 97, True),
+    (9001, 129, True), (4741, 255, False), (5005, 257, True), (4800, 333, True), (4743, 511, True), (4737, 513, True),
+])
+def test_many_rows_of_odd_width(rows, width, affine, dtype):
+    """Enough rows for the kernel that copies 16-byte multiples of rows (and one width past it), the last few alone."""
+    svg2 = require_gpu()
+    X, dY, gamma, beta = make(rows + width, rows, width, dtype, affine)
+    Y, mean, rstd, dX, dgamma, dbeta = both(svg2, X, dY, gamma, beta)
+    ry, rm, rr = forward_ref(X, gamma, beta)
+    check(Y, ry, "Y"), check(mean, rm, "mean"), check(rstd, rr, "rstd")
+    rx, rg, rb = backward_ref(X, dY, gamma, mean, rstd)
+    check(dX, rx, "dX"), check(dgamma, rg, "dgamma"), check(dbeta, rb, "dbeta")
+    again = both(svg2, X, dY, gamma, beta)
+    assert all(torch.equal(p, q) for p, q in zip(again, (Y, mean, rstd, dX, dgamma, dbeta)))
+    buf = X.clone()  # in place, both ways
+    svg2.svg2_layer_norm(buf, gamma, beta, EPS, buf, torch.empty_like(mean), torch.empty_like(rstd))
+    assert torch.equal(buf, Y)
+    ws = svg2.layer_norm_bwd_workspace(rows, width)
+    for into_x in (True, False):
+        x, dy = X.clone(), dY.clone()
+        svg2.svg2_layer_norm_bwd(x, dy, gamma, mean, rstd, x if into_x else dy, torch.empty_like(dgamma), None, ws)
+        assert torch.equal(x if into_x else dy, dX), into_x
