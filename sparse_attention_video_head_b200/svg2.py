@@ -738,8 +738,8 @@ class TrainingLayer:
     selection have no gradient; backward() holds the last forward()'s plan fixed.
 
     Buffers and workspaces are torch tensors owned here; one instance serves one stream at a time, and
-    forward()'s inputs must stay unchanged until backward() has run.  forward() returns the layer's own output
-    buffer, backward() its gradient buffers: the next call overwrites them."""
+    forward()'s inputs and the output it returned must stay unchanged until backward() has run, which reads them.
+    forward() returns the layer's own output buffer, backward() its gradient buffers: the next call overwrites them."""
 
     def __init__(self, B: int, H: int, N: int, d: int, params: Optional[LayerParams] = None,
                  scale: Optional[float] = None, norm_eps: Optional[float] = None, device="cuda"):
@@ -769,6 +769,11 @@ class TrainingLayer:
             self.plan = layer_output_buffers(B, H, N, nQ, nK, device)
         self._kept = None
 
+    def _expect(self, t: Optional[torch.Tensor], name: str):
+        """Another layout of as many elements ([B, N, H, d]) would be read as [B, H, N, d]."""
+        if t is None or tuple(t.shape) != self.shape or t.dtype is not torch.bfloat16:
+            raise ValueError(f"{name}: expected a bf16 tensor of shape {self.shape}")
+
     def forward(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, gamma_q: Optional[torch.Tensor] = None,
                 beta_q: Optional[torch.Tensor] = None, gamma_k: Optional[torch.Tensor] = None,
                 beta_k: Optional[torch.Tensor] = None, uq: Optional[torch.Tensor] = None,
@@ -776,8 +781,7 @@ class TrainingLayer:
         """O for bf16 Q, K, V [B,H,N,d].  init (default params.init): SVG2_INIT_GIVEN starts the k-means from the
         centroids of the last forward()."""
         for t, name in ((Q, "Q"), (K, "K"), (V, "V")):
-            if t is None or tuple(t.shape) != self.shape or t.dtype is not torch.bfloat16:
-                raise ValueError(f"{name}: expected a bf16 tensor of shape {self.shape}")
+            self._expect(t, name)
         if self.norm_eps is None and any(x is not None for x in (gamma_q, beta_q, gamma_k, beta_k)):
             raise ValueError("norm parameters given to a layer without norm_eps")
         self._kept = None
@@ -805,9 +809,11 @@ class TrainingLayer:
         return self.O
 
     def backward(self, dO: torch.Tensor, stream=None) -> Dict[str, torch.Tensor]:
-        """Gradients for the last forward(): dQ, dK, dV of its inputs and, with the norm, dgamma_q, dbeta_q, dgamma_k, dbeta_k."""
+        """Gradients for the last forward(), for bf16 dO [B,H,N,d]: dQ, dK, dV of its inputs and, with the norm, dgamma_q,
+        dbeta_q, dgamma_k, dbeta_k."""
         if self._kept is None:
             raise ValueError("backward() follows a forward()")
+        self._expect(dO, "dO")
         Q, K, V, gamma_q, gamma_k = self._kept
         norm = self.norm_eps is not None
         if self.params is None:

@@ -293,3 +293,24 @@ def test_layer_norm_calls(rec_training):
     for k in ("mean", "rstd", "ws"):
         with pytest.raises(ValueError):
             svg2.svg2_layer_norm_bwd(**{**bwd, k: None})
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+def test_training_layer_backward_refuses_another_layout_of_dO(rec_training, sparse):
+    """dO in any other shape or type than the layer's output is refused, even with the right number of elements: a
+    contiguous [B, N, H, d] would be taken for [B, H, N, d]."""
+    rec = rec_training
+    B, H, N, d = 1, 2, 300, 64
+    t = lambda: _t(B, H, N, d, dtype=bf16)  # noqa: E731
+    prm = svg2.LayerParams(4, 9, 2) if sparse else None
+    layer = svg2.TrainingLayer(B, H, N, d, prm, norm_eps=1e-6, device="cpu")
+    u = dict(uq=_t(B, H, 4, dtype=f64), uk=_t(B, H, 9, dtype=f64)) if sparse else {}
+    layer.forward(t(), t(), t(), **u)
+    n = len(rec.calls)
+    for bad in (_t(B, N, H, d, dtype=bf16), _t(B * H, N, d, dtype=bf16), _t(B * H * N * d, dtype=bf16),
+                _t(2 * B, H, N, d, dtype=bf16), _t(B, H, N, d, dtype=f32), None):
+        with pytest.raises(ValueError):
+            layer.backward(bad)
+    assert len(rec.calls) == n
+    layer.backward(t())
+    assert rec.calls[n][0] == ("svg2_sparse_attn_bwd" if sparse else "svg2_dense_attn_bwd")
