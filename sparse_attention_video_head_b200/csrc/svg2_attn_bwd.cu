@@ -21,8 +21,10 @@
 // A row of dS sums to zero, so dQ does not depend on what all keys have in common; the rounded dS, with delta
 // from a bf16 O, sums to some r_i instead, and dQ would carry scale r_i times that common part, which
 // in a trained K is often its largest.  The query unit therefore sums the dS values it hands over and
-// subtracts scale r_i c, c = the mean key (any c is right in exact arithmetic): on keys with a mean of
-// four standard deviations the error of dQ falls from 1.0e-2 to 2.6e-3 of its norm.
+// subtracts scale r_i c, c = the mean of the keys that the row keeps (any c is right in exact arithmetic): on keys
+// with a mean of four standard deviations the error of dQ falls from 1.0e-2 to 2.6e-3 of its norm.  A mean over other
+// keys too would let large ones among them into rows that do not keep them (one cluster of 40 that is 300 away: dQ off by half
+// its norm), so the sparse call has a mean for every Q cluster.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -122,7 +124,7 @@ struct BwdArgs {
   const int32_t *perm_q, *perm_k;
   const float *neg_lse2, *neg_delta;                   // [BH, N] -lse log2(e), -delta, by permuted row
   const uint4 *lse_step, *delta_step;                  // [BH, N] three_bf16 of -lse / scale, of -delta
-  const float* k_mean;                                 // [BH, D]
+  const float* center;                                 // dense [BH, D], sparse [BH, nQ, D]
   const __nv_bfloat16 *Q, *K, *V, *dO;                 // the tensors of the maps
   __nv_bfloat16 *dQ, *dK, *dV;
   int BH, N, nQ, nK, k_per_head, q_per_head;
@@ -141,22 +143,22 @@ struct BwdBars {
 
 // ------------------------------------------------------------------------------------------------
 // delta_i = dO_i . O_i and the scaled log-sum-exp, by permuted row; with perm, dO's rows in permuted
-// order too.  D / 8 lanes per row, 16 bytes each: bound by the reads of O and dO.  The first BH CTAs take
-// the mean of up to kMeanRows evenly spaced K rows of one plane each.
+// order too.  D / 8 lanes per row, 16 bytes each: bound by the reads of O and dO.  The first CTAs take
+// the mean of up to kMeanRows evenly spaced K rows each, of a plane (dense) or of a K cluster.
 // ------------------------------------------------------------------------------------------------
 constexpr int kMeanRows = 512;
 
 template <int D>
-__device__ void mean_key(const uint4* __restrict__ K, int bh, int N, float* __restrict__ k_mean) {
+__device__ void mean_key(const uint4* __restrict__ K, long long row0, int n, float* __restrict__ mean) {
   constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
   __shared__ float part[kGroups][D];
   const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
-  const int S = min(N, kMeanRows);
+  const int S = min(n, kMeanRows);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 16
   for (int t = group; t < S; t += kGroups) {
-    // floor(t N / S) without a 64-bit division
-    const long long row = static_cast<long long>(bh) * N + t * (N / S) + static_cast<int>(static_cast<unsigned>(t * (N % S)) / static_cast<unsigned>(S));
+    // floor(t n / S) without a 64-bit division
+    const long long row = row0 + t * (n / S) + static_cast<int>(static_cast<unsigned>(t * (n % S)) / static_cast<unsigned>(S));
     const uint4 w = __ldg(K + row * kLanes + sub);
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -173,8 +175,14 @@ __device__ void mean_key(const uint4* __restrict__ K, int bh, int N, float* __re
     float s = 0.f;
     for (int g = 0; g < kGroups; ++g) s += part[g][c];
     s /= static_cast<float>(S);
-    k_mean[static_cast<size_t>(bh) * D + c] = fabsf(s) < INFINITY ? s : 0.f;
+    mean[c] = fabsf(s) < INFINITY ? s : 0.f;
   }
+}
+
+// Rows of cluster i by its plane's offsets; malformed ones hold none.
+__device__ __forceinline__ int cluster_rows(const int32_t* off, int i, int N) {
+  const int start = off[i], n = off[i + 1] - start;
+  return start < 0 || n <= 0 || start > N - n ? 0 : n;
 }
 
 template <int D>
@@ -184,18 +192,29 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
                                                        int BH, float* __restrict__ neg_lse2,
                                                        float* __restrict__ neg_delta, uint4* __restrict__ lse_step,
                                                        uint4* __restrict__ delta_step, float inv_scale,
-                                                       uint4* __restrict__ dOp, float* __restrict__ k_mean,
-                                                       DeviceStatus* st) {
-  if (static_cast<int>(blockIdx.x) < BH) {
-    mean_key<D>(K, blockIdx.x, N, k_mean);
+                                                       uint4* __restrict__ dOp, const int32_t* __restrict__ k_off,
+                                                       int nK, float* __restrict__ means, DeviceStatus* st) {
+  // means: of BH planes (k_off null), or of their nK clusters each; an empty cluster's is not written
+  const unsigned mean_ctas = static_cast<unsigned>(BH) * (k_off != nullptr ? nK : 1);
+  if (blockIdx.x < mean_ctas) {
+    int bh = blockIdx.x, start = 0, n = N;
+    if (k_off != nullptr) {
+      bh = blockIdx.x / nK;
+      const int j = blockIdx.x % nK;
+      const int32_t* off = k_off + static_cast<size_t>(bh) * (nK + 1);
+      start = off[j];
+      n = cluster_rows(off, j, N);
+      if (n == 0) return;
+    }
+    mean_key<D>(K, static_cast<long long>(bh) * N + start, n, means + static_cast<size_t>(blockIdx.x) * D);
     return;
   }
   constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes, kUnroll = 2;
   const int sub = threadIdx.x % kLanes;
   const unsigned total = static_cast<unsigned>(rows);  // below 2^31
-  const unsigned step = (gridDim.x - BH) * 8u * kPerWarp;
+  const unsigned step = (gridDim.x - mean_ctas) * 8u * kPerWarp;
   // every lane of a warp takes part in the shuffles: rows past the end only skip their memory
-  for (unsigned r0 = ((blockIdx.x - BH) * 8u + threadIdx.x / 32) * kPerWarp; r0 < total; r0 += kUnroll * step) {
+  for (unsigned r0 = ((blockIdx.x - mean_ctas) * 8u + threadIdx.x / 32) * kPerWarp; r0 < total; r0 += kUnroll * step) {
     uint4 o[kUnroll], g[kUnroll];
     float l[kUnroll];
     unsigned src[kUnroll];
@@ -324,13 +343,57 @@ constexpr int kPlanRun = 32;  // clusters that one warp packs; units do not cros
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr size_t kPlanSmem = 200 * 1024;  // the selection's bits both ways, if they fit
 
+// The mean of the keys that a Q cluster keeps, from the means of the K clusters: d threads per Q cluster, one
+// per column.  0 for a cluster that keeps none.  list: kPlanThreads entries each of shared memory.
+__device__ void center_clusters(const int32_t* __restrict__ k_off, const int32_t* __restrict__ sel_count,
+                                const int32_t* __restrict__ sel_idx, int N, int nQ, int nK, int d, int rows, int first,
+                                const float* __restrict__ cluster_mean, float* __restrict__ center, int32_t* list,
+                                int32_t* list_rows) {
+  const int col = threadIdx.x % d, group = threadIdx.x / d;
+  const int row = first + group;  // plane * nQ + Q cluster
+  const int bh = row < rows ? row / nQ : 0;
+  const int cnt = row < rows ? min(max(sel_count[row], 0), nK) : 0;
+  const int32_t* off = k_off + static_cast<size_t>(bh) * (nK + 1);
+  const float* means = cluster_mean + static_cast<size_t>(bh) * nK * d + col;
+  float sum = 0.f, n = 0.f;
+  for (int e0 = 0; e0 < nK; e0 += d) {
+    const int e = e0 + col;
+    const int j = e < cnt ? sel_idx[static_cast<size_t>(row) * nK + e] : -1;
+    const int r = j >= 0 && j < nK ? cluster_rows(off, j, N) : 0;
+    list[threadIdx.x] = r > 0 ? j : 0;
+    list_rows[threadIdx.x] = r;
+    __syncthreads();
+    const int most = min(d, cnt - e0);
+#pragma unroll 8
+    for (int t = 0; t < most; ++t) {
+      const int w = list_rows[group * d + t];
+      const float m = w > 0 ? __ldg(means + static_cast<size_t>(list[group * d + t]) * d) : 0.f;
+      sum = fmaf(static_cast<float>(w), m, sum);
+      n += static_cast<float>(w);
+    }
+    __syncthreads();
+  }
+  if (row < rows) {
+    const float c = n > 0.f ? sum / n : 0.f;
+    center[static_cast<size_t>(row) * d + col] = fabsf(c) < INFINITY ? c : 0.f;
+  }
+}
+
+// The first BH CTAs make the plans, the others the means of the kept keys.
 __global__ void __launch_bounds__(kPlanThreads)
     bwd_plan_kernel(const int32_t* __restrict__ q_off, const int32_t* __restrict__ k_off,
                     const int32_t* __restrict__ sel_count, const int32_t* __restrict__ sel_idx, int N, int nQ, int nK,
                     uint32_t* keepers, uint32_t* kept, bool kept_in_smem, BwdUnit* __restrict__ k_units,
-                    int k_per_head, BwdUnit* __restrict__ q_units, int q_per_head, DeviceStatus* st) {
+                    int k_per_head, BwdUnit* __restrict__ q_units, int q_per_head, int BH, int d,
+                    const float* __restrict__ cluster_mean, float* __restrict__ center, DeviceStatus* st) {
   extern __shared__ uint32_t k_bits[];  // [nK, WQ], then [nQ, WK] if it fits, else [32 warps][WK]
   __shared__ int32_t k_offsets[kMaxClustersAssign + 1], q_offsets[kMaxClustersAssign + 1];
+  if (static_cast<int>(blockIdx.x) >= BH) {
+    static_assert(kMaxClustersAssign >= kPlanThreads, "the offsets' arrays hold the lists");
+    center_clusters(k_off, sel_count, sel_idx, N, nQ, nK, d, BH * nQ, (blockIdx.x - BH) * (kPlanThreads / d), cluster_mean,
+                    center, k_offsets, q_offsets);
+    return;
+  }
   const int WQ = (nQ + 31) / 32, WK = (nK + 31) / 32;
   const int bh = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int w = threadIdx.x; w < nK * WQ; w += kPlanThreads) k_bits[w] = 0u;
@@ -405,6 +468,13 @@ struct BwdTmem {
   static constexpr uint32_t acc1 = 128;               // key unit: dV
   static constexpr uint32_t dp = 256, acc2 = 384;     // acc2: dK | dQ
 };
+
+// Which of the unit's clusters a row belongs to, by the offsets of its plane.
+__device__ __forceinline__ int row_segment(const int32_t* off, const BwdUnit un, int row) {
+  int seg = 0;
+  while (seg + 1 < un.nseg && off[un.cluster + seg + 1] <= un.row0 + row) ++seg;
+  return seg;
+}
 
 template <int D, bool DENSE, bool KV, int SPLIT, bool MULTI>
 __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, const BwdUnit un, const int bh,
@@ -856,6 +926,8 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
         if (tk < 0 || tk >= a.N) tk = -1;  // an invalid permutation entry is skipped
       }
       uint4* dst = reinterpret_cast<uint4*>(out + (plane + (tk < 0 ? 0 : tk)) * D);
+      size_t group = bh;  // whose center: the plane's, or the row's Q cluster's
+      if constexpr (!KV && !DENSE) group = static_cast<size_t>(bh) * a.nQ + un.cluster + row_segment(a.q_off + static_cast<size_t>(bh) * (a.nQ + 1), un, row);
 #pragma unroll 1
       for (int c = c0; c < c0 + kChunks; ++c) {
         uint32_t v[32];
@@ -867,7 +939,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
           for (int e = 0; e < 32; ++e) v[e] = 0u;
         }
         if constexpr (!KV) {
-          const float4* mean4 = reinterpret_cast<const float4*>(a.k_mean + static_cast<size_t>(bh) * D + c * 32);
+          const float4* mean4 = reinterpret_cast<const float4*>(a.center + group * D + c * 32);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 m = __ldg(mean4 + e);
@@ -1009,10 +1081,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (warp < 4) {
       const int row = threadIdx.x;
       int seg = 0;  // this row's cluster among the unit's
-      if constexpr (!dense) {
-        const int32_t* off = kv ? a.k_off + static_cast<size_t>(bh) * (a.nK + 1) : a.q_off + static_cast<size_t>(bh) * (a.nQ + 1);
-        while (seg + 1 < un.nseg && off[un.cluster + seg + 1] <= un.row0 + row) ++seg;
-      }
+      if constexpr (!dense)
+        seg = row_segment(kv ? a.k_off + static_cast<size_t>(bh) * (a.nK + 1) : a.q_off + static_cast<size_t>(bh) * (a.nQ + 1), un, row);
       uint32_t w[8] = {0x3f803f80u, 0x3f80u};
 #pragma unroll
       for (int k = 0; k < 6; ++k) w[2 + k] = seg == 2 * k ? 0x3f80u : (seg == 2 * k + 1 ? 0x3f800000u : 0u);
@@ -1071,12 +1141,12 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   const long long rows = static_cast<long long>(BH) * N;
   constexpr int kRows = 256 / (D / 8);  // rows per CTA pass
   const unsigned grid = static_cast<unsigned>(rows / kRows + 1 < 148 * 16 ? rows / kRows + 1 : 148 * 16);
-  bwd_prep_kernel<D><<<grid + BH, 256, 0, s>>>(static_cast<const uint4*>(in.O), static_cast<const uint4*>(in.dO),
+  bwd_prep_kernel<D><<<grid + static_cast<unsigned>(BH) * (dense ? 1 : nK), 256, 0, s>>>(static_cast<const uint4*>(in.O), static_cast<const uint4*>(in.dO),
                                                in.lse, in.perm_q, static_cast<const uint4*>(in.K), N, rows,
                                                BH, sc.neg_lse2, sc.neg_delta,
                                                sc.lse_step, sc.delta_step, 1.f / scale,
                                                in.perm_q != nullptr ? static_cast<uint4*>(sc.dOp) : nullptr,
-                                               sc.k_mean, st);
+                                               dense ? nullptr : in.k_off, nK, dense ? sc.center : sc.cluster_mean, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   BwdArgs a{};
@@ -1091,9 +1161,11 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
     const bool fits = k_bytes + nQ * row <= kPlanSmem;
     e = cudaFuncSetAttribute(bwd_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPlanSmem));
     if (e != cudaSuccess) return e;
-    bwd_plan_kernel<<<BH, kPlanThreads, k_bytes + (fits ? nQ : kPlanWarps) * row, s>>>(
+    constexpr int kCenters = kPlanThreads / D;  // Q clusters per CTA
+    const unsigned plan_grid = static_cast<unsigned>(BH + (static_cast<long long>(BH) * nQ + kCenters - 1) / kCenters);
+    bwd_plan_kernel<<<plan_grid, kPlanThreads, k_bytes + (fits ? nQ : kPlanWarps) * row, s>>>(
         in.q_off, in.k_off, in.sel_count, in.sel_idx, N, nQ, nK, sc.keepers, sc.kept, fits, sc.k_units, a.k_per_head,
-        sc.q_units, a.q_per_head, st);
+        sc.q_units, a.q_per_head, BH, D, sc.cluster_mean, sc.center, st);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -1107,7 +1179,7 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   a.perm_k = in.perm_k;
   a.neg_lse2 = sc.neg_lse2;
   a.neg_delta = sc.neg_delta;
-  a.k_mean = sc.k_mean;
+  a.center = sc.center;
   a.lse_step = sc.lse_step;
   a.delta_step = sc.delta_step;
   a.dQ = static_cast<__nv_bfloat16*>(in.dQ);

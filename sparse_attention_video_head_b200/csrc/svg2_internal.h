@@ -216,7 +216,8 @@ inline int bwd_max_units_per_head(int N, int n) { return N / 128 + n; }
 struct BwdScratch {
   float *neg_lse2, *neg_delta;  // [BH, N] -lse log2(e) and -dO.O by permuted row
   uint4 *lse_step, *delta_step;  // [BH, N] -lse / scale and -delta as three bf16 each
-  float* k_mean;                // [BH, d] mean of (a sample of) the plane's K rows
+  float* center;                // what dQ's key sums are taken about: dense [BH, d], sparse [BH, nQ, d]
+  float* cluster_mean;          // [BH, nK, d] mean of (up to 512 of) a K cluster's rows
   void* dOp;                    // [BH, N, d] dO in permuted order (used when perm_q is given)
   uint32_t* keepers;            // [BH, nK, ceil(nQ / 32)] bit i: Q cluster i keeps the K cluster
   uint32_t* kept;               // [BH, nQ, ceil(nK / 32)] bit j: the Q cluster keeps K cluster j
@@ -230,7 +231,8 @@ inline void carve_bwd(Carve& c, int BH, int N, int d, int nQ, int nK, BwdScratch
   s.neg_delta = c.take<float>(rows);
   s.lse_step = c.take<uint4>(rows);
   s.delta_step = c.take<uint4>(rows);
-  s.k_mean = c.take<float>(static_cast<size_t>(BH) * d);
+  s.center = c.take<float>(static_cast<size_t>(BH) * (nQ > 0 ? nQ : 1) * d);
+  s.cluster_mean = nQ > 0 ? c.take<float>(static_cast<size_t>(BH) * nK * d) : nullptr;
   s.dOp = nQ > 0 ? c.take<uint16_t>(rows * d) : nullptr;
   s.keepers = nQ > 0 ? c.take<uint32_t>(static_cast<size_t>(BH) * nK * ((nQ + 31) / 32)) : nullptr;
   s.kept = nQ > 0 ? c.take<uint32_t>(static_cast<size_t>(BH) * nQ * ((nK + 31) / 32)) : nullptr;

@@ -568,3 +568,64 @@ def test_malformed_offsets_stay_in_their_planes():
     svg2.raise_on_device_error(ws)
     for n, x in zip(("dQ", "dK", "dV"), grads):
         assert torch.equal(x[0, 0], ref[n][0, 0]), n
+
+
+def even_plan(seed, B, H, N, nQ, nK, keep):
+    """Clusters of about equal size, keep [nQ, nK] for every plane, no permutations."""
+    edges = lambda n: torch.tensor([N * i // n for i in range(n + 1)], dtype=torch.int32, device="cuda")  # noqa: E731
+    keep = keep.to("cuda").expand(B, H, nQ, nK).contiguous()
+    return dict(q_off=edges(nQ).expand(B, H, nQ + 1).contiguous(), k_off=edges(nK).expand(B, H, nK + 1).contiguous(),
+                keep=keep, sel_count=keep.sum(3, dtype=torch.int32),
+                sel_idx=torch.sort(keep.to(torch.uint8), dim=3, descending=True, stable=True).indices.int().contiguous())
+
+
+def rel_norm(x, ref):
+    return (torch.linalg.norm(x.double() - ref) / torch.linalg.norm(ref)).item()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,nQ,d", [(5000, 100, 64), (5000, 5, 128), (1000, 20, 64), (400, 2, 128)])
+def test_large_keys_cost_nothing_to_rows_that_do_not_keep_them(N, nQ, d):
+    """K clusters 7 and 30 hold finite keys 300 past the others in every column; the odd Q clusters keep neither (30
+    is kept by none), and the last rows of the plane, in no cluster, are larger still.  The dS that is handed over sums to
+    some r_i, so what dQ subtracts has to come from the keys that the row keeps: the limit is the one of
+    the other tests, 2 U for roundings of independent sign, and does not know the large keys.  Units hold rows of one
+    cluster (nQ small) and of odd and even ones."""
+    svg2 = require_gpu()
+    g = gen(N + nQ)
+    Q, K, V, dO = (randn(g, 1, 1, N, d) for _ in range(4))
+    nK = 40
+    keep = torch.ones(nQ, nK, dtype=torch.bool)
+    keep[:, 30] = False
+    keep[1::2, 7] = False
+    pl = even_plan(0, 1, 1, N, nQ, nK, keep)
+    end = N - N // 50  # rows past the last cluster
+    pl["k_off"].clamp_(max=end)
+    for c, x in ((7, 300.0), (30, 300.0)):
+        K[0, 0, pl["k_off"][0, 0, c]:pl["k_off"][0, 0, c + 1]] += x
+    K[0, 0, end:] = 1e4
+    got = sparse_step(svg2, pl, Q, K, V, dO, d ** -0.5, perms=False)
+    rows = torch.cat([torch.arange(pl["q_off"][0, 0, c].item(), pl["q_off"][0, 0, c + 1].item(), device="cuda") for c in range(1, nQ, 2)])
+    cols = torch.cat([torch.arange(pl["k_off"][0, 0, c].item(), pl["k_off"][0, 0, c + 1].item(), device="cuda") for c in range(nK) if c not in (7, 30)])
+    ref, _ = formulas(Q[0, 0, rows], K[0, 0, cols], V[0, 0, cols], dO[0, 0, rows], d ** -0.5)
+    for n in ("O", "dQ"):
+        assert rel_norm(got[n][0, 0, rows], ref[n]) <= 2 * U, (n, rel_norm(got[n][0, 0, rows], ref[n]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,nQ,nK,mean", [(5000, 100, 40, 4.0), (5000, 5, 3, 4.0), (2000, 40, 2, 30.0)])
+def test_what_the_kept_keys_have_in_common_costs_little(N, nQ, nK, mean):
+    """Keys with a large mean of their own in every K cluster: dQ subtracts the kept keys' mean.  With c that mean, an
+    error e_ij of dS enters as e_ij (k_j - c): the keys' spread counts, their mean does not; the limit is 2 U.  K clusters
+    of up to 512 rows have their exact mean, longer ones that of 512 evenly spaced rows."""
+    svg2 = require_gpu()
+    g = gen(N + nK)
+    Q, K, V, dO = (randn(g, 1, 1, N, 64) for _ in range(4))
+    K = (K.float() + mean).bfloat16()
+    keep = torch.ones(nQ, nK, dtype=torch.bool)
+    keep[1, 0] = False
+    pl = even_plan(0, 1, 1, N, nQ, nK, keep)
+    scale = 0.125 / mean
+    got = sparse_step(svg2, pl, Q, K, V, dO, scale, perms=False)
+    ref, _ = formulas(Q[0, 0], K[0, 0], V[0, 0], dO[0, 0], scale, rows_kept(pl, 0, 0, N))
+    assert rel_norm(got["dQ"][0, 0], ref["dQ"]) <= 2 * U, rel_norm(got["dQ"][0, 0], ref["dQ"])
