@@ -388,6 +388,7 @@ __global__ void __launch_bounds__(kPlanThreads)
                     const float* __restrict__ cluster_mean, float* __restrict__ center, DeviceStatus* st) {
   extern __shared__ uint32_t k_bits[];  // [nK, WQ], then [nQ, WK] if it fits, else [32 warps][WK]
   __shared__ int32_t k_offsets[kMaxClustersAssign + 1], q_offsets[kMaxClustersAssign + 1];
+  __shared__ uint32_t k_rows[kPlanWarps], q_rows[kPlanWarps];  // the clusters that have rows
   if (static_cast<int>(blockIdx.x) >= BH) {
     static_assert(kMaxClustersAssign >= kPlanThreads, "the offsets' arrays hold the lists");
     center_clusters(k_off, sel_count, sel_idx, N, nQ, nK, d, BH * nQ, (blockIdx.x - BH) * (kPlanThreads / d), cluster_mean,
@@ -403,6 +404,14 @@ __global__ void __launch_bounds__(kPlanThreads)
   for (int i = threadIdx.x; i < q_per_head; i += kPlanThreads) qu[i] = BwdUnit{0, 0, 0, 0};
   for (int i = threadIdx.x; i <= nK; i += kPlanThreads) k_offsets[i] = k_off[static_cast<size_t>(bh) * (nK + 1) + i];
   for (int i = threadIdx.x; i <= nQ; i += kPlanThreads) q_offsets[i] = q_off[static_cast<size_t>(bh) * (nQ + 1) + i];
+  __syncthreads();
+  {
+    static_assert(kMaxClustersAssign <= kPlanThreads, "a thread per cluster");
+    const int c = threadIdx.x;
+    const uint32_t k = __ballot_sync(0xffffffffu, c < nK && cluster_rows(k_offsets, c, N) > 0);
+    const uint32_t q = __ballot_sync(0xffffffffu, c < nQ && cluster_rows(q_offsets, c, N) > 0);
+    if (lane == 0) k_rows[warp] = k, q_rows[warp] = q;
+  }
   __syncthreads();
   uint32_t* kept_g = kept + static_cast<size_t>(bh) * nQ * WK;
   uint32_t* q_bits_s = k_bits + nK * WQ;
@@ -431,11 +440,19 @@ __global__ void __launch_bounds__(kPlanThreads)
       }
     }
     __syncwarp();
-    for (int w = lane; w < WK; w += 32) kept_g[i * WK + w] = mine[w];
+    // Clusters without rows keep nothing and are kept by nothing: a unit may span an empty cluster, whose part of the
+    // selection would lengthen its stream, and the packing counts bits.
+    const bool has = (q_rows[i >> 5] >> (i & 31)) & 1u;
+    for (int w = lane; w < WK; w += 32) kept_g[i * WK + w] = mine[w] = has ? mine[w] & k_rows[w] : 0u;
     __syncwarp();
   }
   __syncthreads();
-  for (int w = threadIdx.x; w < nK * WQ; w += kPlanThreads) keepers[static_cast<size_t>(bh) * nK * WQ + w] = k_bits[w];
+  for (int w = threadIdx.x; w < nK * WQ; w += kPlanThreads) {
+    const int j = w / WQ;
+    const bool has = (k_rows[j >> 5] >> (j & 31)) & 1u;
+    keepers[static_cast<size_t>(bh) * nK * WQ + w] = k_bits[w] = has ? k_bits[w] & q_rows[w - j * WQ] : 0u;
+  }
+  __syncthreads();
   // units: a run's go from the slot that the runs before it cannot reach (a run of n clusters and m rows has at
   // most n + m / 128), the slots between stay empty
   const int runs_k = (nK + kPlanRun - 1) / kPlanRun, runs_q = (nQ + kPlanRun - 1) / kPlanRun;

@@ -629,3 +629,42 @@ def test_what_the_kept_keys_have_in_common_costs_little(N, nQ, nK, mean):
     got = sparse_step(svg2, pl, Q, K, V, dO, scale, perms=False)
     ref, _ = formulas(Q[0, 0], K[0, 0], V[0, 0], dO[0, 0], scale, rows_kept(pl, 0, 0, N))
     assert rel_norm(got["dQ"][0, 0], ref["dQ"]) <= 2 * U, rel_norm(got["dQ"][0, 0], ref["dQ"])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [600, 5000])
+def test_what_an_empty_cluster_keeps_changes_nothing(N):
+    """Empty Q clusters between small ones, and empty K clusters: their part of the selection has no rows.  With all of
+    it listed and with none the gradients have the same bits, and NaN that only empty clusters keep reaches nothing."""
+    svg2 = require_gpu()
+    B, H, d, n = 1, 2, 64, 41
+    g = gen(N + 1)
+    Q, K, V, dO = (randn(g, B, H, N, d) for _ in range(4))
+    rng = np.random.default_rng(N)
+    keep = torch.from_numpy(rng.random((n, n)) < 0.3)
+    empty = torch.arange(n) % 2 == 1
+    at = [0]  # the odd clusters are empty
+    for i in range(n):
+        at.append(at[-1] if i % 2 else N * (i // 2 + 1) // 21)
+    got = []
+    for listed in (False, True):
+        k = keep.clone()
+        k[empty], k[:, empty] = listed, listed
+        k[~empty, 6] = False  # the rows of K cluster 6 and of Q cluster 8: kept by empty clusters alone
+        k[8, ~empty] = False
+        pl = even_plan(0, B, H, N, n, n, k)
+        pl["q_off"] = pl["k_off"] = torch.tensor(at, dtype=torch.int32, device="cuda").expand(B, H, n + 1).contiguous()
+        got.append(sparse_step(svg2, pl, Q, K, V, dO, 0.125, perms=False))
+    assert same(*got)
+    K[:, :, at[6]:at[7]] = torch.nan
+    V[:, :, at[6]:at[7]] = torch.inf
+    Q[:, :, at[8]:at[9]] = torch.nan
+    dO[:, :, at[8]:at[9]] = torch.nan
+    bad = sparse_step(svg2, pl, Q, K, V, dO, 0.125, perms=False)
+    rows = torch.ones(N, dtype=torch.bool, device="cuda")
+    rows[at[8]:at[9]] = False
+    assert torch.equal(bad["dQ"][:, :, rows], got[1]["dQ"][:, :, rows])
+    rows[:] = True
+    rows[at[6]:at[7]] = False
+    for m in ("dK", "dV"):
+        assert torch.equal(bad[m][:, :, rows], got[1][m][:, :, rows]), m
