@@ -244,6 +244,8 @@ SVG2_API int svg2_dense_attn(const void* Q, const void* K, const void* V, int B,
  * workspace, errors and O, bit for bit) that also write
  *   lse      float [B,H,N], out: lse_i = log sum_j exp(scale * q_i.k_j) over the row's keys, indexed by
  *            (permuted) row, whether perm_q is given or not; -inf for a row that keeps no key (O is 0).
+ *            Its absolute error is at most 7.5e-5 beside the scores' own float32 rounding (the exponentials of a quarter of the
+ *            keys are a cubic's); a NaN key of that quarter counts as one that is not there, in O as in lse.
  * Here and in the gradient calls scale must be finite and at least 1e-30 (else SVG2_ERR_INVALID_ARG). */
 SVG2_API int svg2_dense_attn_lse(const void* Q, const void* K, const void* V, int B, int H, int N, int d, float scale,
                                  void* O, float* lse, void* ws, size_t ws_bytes, void* stream);
@@ -260,8 +262,8 @@ SVG2_API int svg2_sparse_attn_lse(const void* Qp, const void* Kp, const void* Vp
  *   ws              at least svg2_dense_attn_bwd_workspace_size() bytes, 256-byte aligned (enough for
  *                   svg2_dense_attn_lse too); holds the status word.
  * P and dS are rounded to bf16 for the products, sums are float32; the results are the same on every run.
- * A NaN or infinity in a row reaches the gradients of the rows it shares a key or query with.  Errors as
- * svg2_dense_attn. */
+ * A NaN in a row of Q, K, V, dO or lse reaches every gradient whose formula holds it, also where the forward left a
+ * NaN key out; so does an infinity, but where its score is -inf, which is a P of 0.  Errors as svg2_dense_attn. */
 SVG2_API int svg2_dense_attn_bwd_workspace_size(int B, int H, int N, int d, size_t* bytes);
 SVG2_API int svg2_dense_attn_bwd(const void* Q, const void* K, const void* V, const void* O, const float* lse,
                                  const void* dO, int B, int H, int N, int d, float scale, void* dQ, void* dK,

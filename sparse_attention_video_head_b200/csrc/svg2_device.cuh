@@ -361,18 +361,30 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 // iteratively reweighted least squares: 7.5e-5 in float32, far below the bf16 rounding of P), and
 // 2^n enters by adding n to the exponent field.  x is clamped at -126, where 2^x is below every
 // other term of a softmax row.
-__device__ __forceinline__ float2 exp2_cubic2(float2 x) {
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
-  const float2 t = add2(x, make_float2(12582912.f, 12582912.f));
+__device__ __forceinline__ float2 exp2_cubic_parts2(float2 x, float2& t) {  // 2^f; n in t's low bits
+  t = add2(x, make_float2(12582912.f, 12582912.f));
   const float2 n = add2(t, make_float2(-12582912.f, -12582912.f));
   const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
   float2 p = fma2(make_float2(0.05517150089144707f, 0.05517150089144707f), f,
                   make_float2(0.24261096119880676f, 0.24261096119880676f));
   p = fma2(p, f, make_float2(0.6932609677314758f, 0.6932609677314758f));
-  p = fma2(p, f, make_float2(0.9999280571937561f, 0.9999280571937561f));
+  return fma2(p, f, make_float2(0.9999280571937561f, 0.9999280571937561f));
+}
+__device__ __forceinline__ float2 exp2_cubic2(float2 x) {
+  float2 t;
+  const float2 p = exp2_cubic_parts2(make_float2(fmaxf(x.x, -126.f), fmaxf(x.y, -126.f)), t);
   return make_float2(__uint_as_float(__float_as_uint(t.x) * 8388608u + __float_as_uint(p.x)),
                      __uint_as_float(__float_as_uint(t.y) * 8388608u + __float_as_uint(p.y)));
+}
+// The same values, and NaN for NaN: above, the clamp takes a NaN for -126 and the exponent's addition would turn one
+// into a number.
+__device__ __forceinline__ float2 exp2_cubic2_nan(float2 x) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-126.f));
+  float2 t;
+  const float2 p = exp2_cubic_parts2(x, t);
+  return mul2(p, make_float2(__uint_as_float(__float_as_uint(t.x) * 8388608u + 0x3f800000u),
+                             __uint_as_float(__float_as_uint(t.y) * 8388608u + 0x3f800000u)));
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {

@@ -668,3 +668,27 @@ def test_what_an_empty_cluster_keeps_changes_nothing(N):
     rows[at[6]:at[7]] = False
     for m in ("dK", "dV"):
         assert torch.equal(bad[m][:, :, rows], got[1][m][:, :, rows]), m
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [300, 700, 4200])
+@pytest.mark.parametrize("at", [5, 20])
+def test_dense_nan_reaches_every_row_it_shares_a_pair_with(N, at):
+    """A NaN query, key, value or gradient row, at places that each way of taking 2^x has: every gradient whose formula
+    has it is NaN, in all its entries; the other queries' dQ keep their bits where only a query's row is NaN."""
+    svg2 = require_gpu()
+    g = gen(N)
+    x = {n: randn(g, 1, 1, N, 64) for n in ("Q", "K", "V", "dO")}
+    ref = dense_step(svg2, *x.values(), 0.125)
+    others = torch.arange(N, device="cuda") != at
+    for n, reached in (("Q", ("dK", "dV")), ("dO", ("dK", "dV")), ("K", ("dQ",)), ("V", ("dQ", "dK"))):
+        bad = {m: t.clone() for m, t in x.items()}
+        bad[n][0, 0, at] = torch.nan
+        got = dense_step(svg2, *bad.values(), 0.125)
+        for m in reached:
+            assert torch.isnan(got[m]).all(), (n, m, torch.isnan(got[m]).float().mean().item())
+        if n in ("Q", "dO"):
+            assert torch.isnan(got["dQ"][0, 0, at]).all()
+            assert torch.equal(got["dQ"][0, 0, others], ref["dQ"][0, 0, others]), n
+        if n == "K":
+            assert torch.isnan(got["dK"][0, 0, at]).all() and torch.isnan(got["dV"][0, 0, at]).all()
