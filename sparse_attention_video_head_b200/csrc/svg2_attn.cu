@@ -73,7 +73,9 @@ struct AttnBars {
   int32_t nranges;
 };
 
-__global__ void plan_count_kernel(const int32_t* __restrict__ q_off, int nQ, int N,
+// `most`: the room per head.  Offsets that ascend never need more; others may overlap, and what they have past it is
+// left out, so that a head writes its own part of the list alone.
+__global__ void plan_count_kernel(const int32_t* __restrict__ q_off, int nQ, int N, int most,
                                   int32_t* __restrict__ head_units, DeviceStatus* st) {
   __shared__ int32_t part[32];
   const int bh = blockIdx.x;
@@ -92,7 +94,7 @@ __global__ void plan_count_kernel(const int32_t* __restrict__ q_off, int nQ, int
   if (threadIdx.x == 0) {
     int t = 0;
     for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) t += part[w];
-    head_units[bh] = t;
+    head_units[bh] = min(t, most);
   }
 }
 
@@ -112,11 +114,12 @@ __global__ void plan_write_kernel(const int32_t* __restrict__ q_off, int nQ, int
   const int bh = blockIdx.x;
   if (threadIdx.x != 0) return;
   int pos = head_base[bh];
+  const int end = head_base[bh + 1];
   const int32_t* qo = q_off + static_cast<size_t>(bh) * (nQ + 1);
   for (int i = 0; i < nQ; ++i) {
     const int r0 = qo[i], n = qo[i + 1] - qo[i];
     if (r0 < 0 || n <= 0 || r0 + n > N) continue;  // malformed offsets produce no work
-    for (int u = 0; u < n; u += 256) {
+    for (int u = 0; u < n && pos < end; u += 256) {
       AttnUnit un;
       un.bh = bh;
       un.cluster = i;
@@ -855,7 +858,7 @@ cudaError_t launch_attn_plan(const int32_t* q_off, int BH, int N, int nQ, const 
                                                         BH * attn_lse_units_per_head(BH, N, nQ), st);
     return cudaGetLastError();
   }
-  plan_count_kernel<<<BH, 256, 0, s>>>(q_off, nQ, N, sc.head_units, st);
+  plan_count_kernel<<<BH, 256, 0, s>>>(q_off, nQ, N, attn_max_units_per_head(N, nQ), sc.head_units, st);
   plan_scan_kernel<<<1, 32, 0, s>>>(sc.head_units, BH, sc.head_base);
   plan_write_kernel<<<BH, 32, 0, s>>>(q_off, nQ, N, sc.head_base, sc.units);
   return cudaGetLastError();

@@ -692,3 +692,34 @@ def test_dense_nan_reaches_every_row_it_shares_a_pair_with(N, at):
             assert torch.equal(got["dQ"][0, 0, others], ref["dQ"][0, 0, others]), n
         if n == "K":
             assert torch.isnan(got["dK"][0, 0, at]).all() and torch.isnan(got["dV"][0, 0, at]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,N,nQ", [(17, 1100, 1024), (3, 3000, 200), (2, 20000, 40)])
+def test_forward_plans_of_overlapping_clusters_stay_in_their_room(H, N, nQ):
+    """Offsets of one plane that go up and down between 0 and N hold many more units than the plan has room for: what
+    stands behind its part of the workspace and behind the workspace stays, and the other planes' rows are what they
+    were (17 planes of 1024 clusters are planned by the kernels of large plans, with log-sum-exp too)."""
+    svg2 = require_gpu()
+    g = gen(33)
+    d, nK = 64, 30
+    Q, K, V = (randn(g, 1, H, N, d) for _ in range(3))
+    pl = plan(34, 1, H, N, nQ, nK, 0.5)
+    args = [pl[n] for n in ("q_off", "k_off", "sel_count", "sel_idx")]
+    bad = [args[0].clone(), *args[1:]]
+    bad[0][0, H - 1] = torch.arange(nQ + 1, device="cuda", dtype=torch.int32) % 2 * N
+    for lse in (None, torch.full((1, H, N), torch.nan, device="cuda")):
+        size = (svg2.svg2_workspace_size if lse is None else svg2.svg2_sparse_attn_bwd_workspace_size)(1, H, N, d, nQ, nK)
+        out = []
+        for a in (args, bad):
+            room = torch.full((size + (1 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+            room[:256] = 0
+            O = torch.zeros_like(Q)
+            if lse is None:
+                svg2.svg2_sparse_attn(Q, K, V, *a, 0.1, O, room[:size])
+            else:
+                svg2.svg2_sparse_attn_lse(Q, K, V, *a, 0.1, O, lse, room[:size])
+            svg2.raise_on_device_error(room[:size])
+            assert (room[size:] == 0x5a).all()
+            out.append((O[:, :H - 1], None if lse is None else lse[:, :H - 1].clone()))
+        assert torch.equal(out[0][0], out[1][0]) and (lse is None or torch.equal(out[0][1], out[1][1]))
