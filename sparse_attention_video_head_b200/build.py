@@ -5,6 +5,7 @@ import glob
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -40,13 +41,14 @@ def _stale(out: str, deps) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False, debug: bool = False) -> str:
-    """Compile libsvg2.so (or, with debug=True, libsvg2_debug.so) in-tree; returns the library's path."""
+    """Compile libsvg2.so (or, with debug=True, libsvg2_debug.so) in-tree, the stale sources side by side (the attention
+    gradients alone take more than half of the time); returns the library's path."""
     out_dir = os.path.join(BUILD_DIR, "debug") if debug else BUILD_DIR
     lib = DEBUG_LIB if debug else LIB
     os.makedirs(out_dir, exist_ok=True)
     headers = glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
-    objs = []
+    objs, cmds = [], []
     for src in sources():
         obj = os.path.join(out_dir, os.path.basename(src).replace(".cu", ".o"))
         objs.append(obj)
@@ -56,7 +58,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
                 cmd += ["-Xptxas", "-v"]
             if verbose:
                 print(" ".join(cmd), file=sys.stderr)
-            subprocess.check_call(cmd)
+            cmds.append(cmd)
+    with ThreadPoolExecutor(max(1, min(len(cmds), os.cpu_count() or 1))) as pool:
+        list(pool.map(subprocess.check_call, cmds))  # (the first failure is raised here)
     if force or _stale(lib, objs):
         cmd = [_nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", lib, *objs]
         if verbose:
