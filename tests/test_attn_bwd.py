@@ -4,8 +4,9 @@ Tolerances, elementwise, from the formulas (u = 2^-8, half a bf16 step).  A prob
 error of at most EP: the cubic exponential's 7.5e-5, twice (once in P, once in lse), and the error of
 a float32 score, at most (d + 2) 2^-24 scale sum |q k|, twice.  P and dS are rounded to bf16, O too
 (it enters delta = dO.O), and the outputs.  dQ is summed as scale sum_j dS_ij (k_j - c) with c the mean of up to
-512 evenly spaced keys (the same in exact arithmetic, where a row of dS sums to zero), so an error e_ij of dS
-enters as e_ij (k_j - c), and the float32 sums over N keys add N 2^-24 times their terms' magnitudes (which the
+512 evenly spaced keys, or of the keys that the row's cluster keeps in the sparse call (the same in exact arithmetic,
+where a row of dS sums to zero; formulas() takes the first for both, which for keys of one distribution is as far
+from them), so an error e_ij of dS enters as e_ij (k_j - c), and the float32 sums over N keys add N 2^-24 times their terms' magnitudes (which the
 bf16 terms cover everywhere else).  With |.| taken inside every sum this bounds each entry; for
 errors of independent sign the relative 2-norm stays below 2 u, which is checked where the sums do not cancel."""
 import numpy as np
@@ -723,3 +724,40 @@ def test_forward_plans_of_overlapping_clusters_stay_in_their_room(H, N, nQ):
             assert (room[size:] == 0x5a).all()
             out.append((O[:, :H - 1], None if lse is None else lse[:, :H - 1].clone()))
         assert torch.equal(out[0][0], out[1][0]) and (lse is None or torch.equal(out[0][1], out[1][1]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,H,N,d", [(1, 2, 4096, 64), (1, 1, 4097, 128), (1, 1, 4097, 64), (2, 1, 4500, 128), (1, 1, 5003, 64)])
+def test_dense_gradients_of_long_rows(B, H, N, d):
+    """The last length whose query units hand half of dS over as two numbers, and longer ones, which have a kernel of
+    their own; 33 tiles and more, so every stage is reused many times."""
+    test_dense_gradients(B, H, N, d)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nQ,nK", [(2, 3), (100, 90), (100, 3), (2, 90)])
+def test_sparse_gradients_of_long_streams(nQ, nK, d):
+    """Streams of more than 4096 rows, for units inside one cluster (few clusters) and over several (many), for
+    queries and keys each: the variants without split hand-over."""
+    test_sparse_gradients(1, 1, 5500, d, nQ, nK, 0.97, {}, True)
+
+
+@pytest.mark.gpu
+def test_sparse_wait_that_runs_out_is_reported_and_leaves_the_workspace_usable():
+    """The same as for the dense call, through the gathering producers: tiles of one piece and of many."""
+    svg2 = require_gpu()
+    g = gen(31)
+    B, H, N, d = 1, 2, 1000, 128
+    Q, K, V, dO = (randn(g, B, H, N, d) for _ in range(4))
+    for nQ, nK in ((3, 4), (60, 50)):
+        pl = plan(32 + nQ, B, H, N, nQ, nK, 0.7)
+        want = sparse_step(svg2, pl, Q, K, V, dO, 0.1)
+        ws = svg2.sparse_bwd_workspace(B, H, N, d, nQ, nK)
+        grads = [torch.empty_like(Q) for _ in range(3)]
+        svg2.svg2_set_wait_budget(ws, 1)
+        svg2.svg2_sparse_attn_bwd(Q, K, V, want["O"], want["lse"], dO, *(pl[n] for n in ("q_off", "k_off", "sel_count", "sel_idx")),
+                                  0.1, *grads, ws, perm_q=pl["perm_q"], perm_k=pl["perm_k"])
+        assert svg2.svg2_check_status(ws)[0] == 5
+        svg2.svg2_set_wait_budget(ws, 0)
+        assert same(sparse_step(svg2, pl, Q, K, V, dO, 0.1, ws=ws), want)
