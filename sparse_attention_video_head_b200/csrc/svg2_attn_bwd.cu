@@ -73,12 +73,13 @@ constexpr uint32_t kSegPenalty = 0xff7fu;  // bf16 -3.39e38
 // of the tile, T2 only from dP (to dV), so three and one let T1 arrive a period early: 8 x 12480 x 128 takes 1.75 ms
 // against 1.92 with two of each.  (At d = 64 more would fit; four of each gained nothing.)
 constexpr int kStages1 = 3, kStages2 = 1, kStreamTiles = kStages1 + kStages2;
+constexpr uint32_t kBarBytes = 384;  // barriers, and what else a CTA shares
 
 template <int D>
 constexpr uint32_t bwd_smem() {
   return (2 + kStreamTiles) * bwd_tile_bytes<D>() + 1024 /*align*/ + 2048 /*row sums*/ + 4096 /*range starts*/ +
          4096 + 64 /*range offsets*/ + 2048 /*range segments*/ + (1 + kStreamTiles) * kStepBytes /*A, B of S and dP by stage*/ +
-         256 /*barriers*/;
+         kBarBytes;
 }
 static_assert(bwd_smem<128>() <= 227 * 1024, "shared memory");
 
@@ -137,8 +138,10 @@ struct BwdBars {
   uint64_t res_full, t1_full[kStages1], t2_full[kStages2], t1_empty[kStages1], t2_empty[kStages2], s_full[2], p_full[2], dp_full, ds_full[2], o_full,
       mma_done;
   uint32_t tmem_base;
-  int32_t L, nranges;
+  int32_t L;
+  uint8_t seg[128];  // sparse query unit: each row's cluster, counted from the unit's first
 };
+static_assert(sizeof(BwdBars) <= kBarBytes, "shared memory");
 
 
 // ------------------------------------------------------------------------------------------------
@@ -147,16 +150,20 @@ struct BwdBars {
 // the mean of up to kMeanRows evenly spaced K rows each, of a plane (dense) or of a K cluster.
 // ------------------------------------------------------------------------------------------------
 constexpr int kMeanRows = 512;
+// From this many rows per K cluster on a CTA takes a cluster's mean, below a warp does (gradients of 24 x 4096 x 128 in 1024
+// clusters: 1490 us with warps, 1537 with CTAs; 1 x 4096 x 64 in 32: 71.2 with warps, 66.8 with CTAs).
+constexpr int kMeanWide = 64;
 
+// W warps (all eight, or one each) per mean: of rows row0 .. row0 + n - 1 (n = 0: not written).
 template <int D>
-__device__ void mean_key(const uint4* __restrict__ K, long long row0, int n, float* __restrict__ mean) {
-  constexpr int kLanes = D / 8, kGroups = 256 / kLanes;
+__device__ void mean_key(const uint4* __restrict__ K, long long row0, int n, int W, float* __restrict__ mean) {
+  constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes, kGroups = 256 / kLanes;
   __shared__ float part[kGroups][D];
-  const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes, groups = W * kPerWarp;
   const int S = min(n, kMeanRows);
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 16
-  for (int t = group; t < S; t += kGroups) {
+  for (int t = group % groups; t < S; t += groups) {
     // floor(t n / S) without a 64-bit division
     const long long row = row0 + t * (n / S) + static_cast<int>(static_cast<unsigned>(t * (n % S)) / static_cast<unsigned>(S));
     const uint4 w = __ldg(K + row * kLanes + sub);
@@ -171,9 +178,11 @@ __device__ void mean_key(const uint4* __restrict__ K, long long row0, int n, flo
 #pragma unroll
   for (int e = 0; e < 8; ++e) part[group][sub * 8 + e] = acc[e];
   __syncthreads();
-  for (int c = threadIdx.x; c < D; c += 256) {
+  if (n == 0) return;
+  const int first = group / groups * groups;  // of the partial sums of this thread's mean
+  for (int c = threadIdx.x % (32 * W); c < D; c += 32 * W) {
     float s = 0.f;
-    for (int g = 0; g < kGroups; ++g) s += part[g][c];
+    for (int g = 0; g < groups; ++g) s += part[first + g][c];
     s /= static_cast<float>(S);
     mean[c] = fabsf(s) < INFINITY ? s : 0.f;
   }
@@ -185,6 +194,11 @@ __device__ __forceinline__ int cluster_rows(const int32_t* off, int i, int N) {
   return start < 0 || n <= 0 || start > N - n ? 0 : n;
 }
 
+__host__ __device__ __forceinline__ unsigned mean_ctas_of(int BH, int n, int mean_warps) {
+  const unsigned count = static_cast<unsigned>(BH) * n;
+  return mean_warps == 8 ? count : (count + 7) / 8;
+}
+
 template <int D>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__ O, const uint4* __restrict__ dO,
                                                        const float* __restrict__ lse, const int32_t* __restrict__ perm,
@@ -193,20 +207,22 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__
                                                        float* __restrict__ neg_delta, uint4* __restrict__ lse_step,
                                                        uint4* __restrict__ delta_step, float inv_scale,
                                                        uint4* __restrict__ dOp, const int32_t* __restrict__ k_off,
-                                                       int nK, float* __restrict__ means, DeviceStatus* st) {
-  // means: of BH planes (k_off null), or of their nK clusters each; an empty cluster's is not written
-  const unsigned mean_ctas = static_cast<unsigned>(BH) * (k_off != nullptr ? nK : 1);
+                                                       int nK, int mean_warps, float* __restrict__ means,
+                                                       DeviceStatus* st) {
+  // means: of BH planes (k_off null), or of their nK clusters each, eight to a CTA where mean_warps is 1
+  const unsigned mean_ctas = mean_ctas_of(BH, k_off != nullptr ? nK : 1, mean_warps);
   if (blockIdx.x < mean_ctas) {
-    int bh = blockIdx.x, start = 0, n = N;
-    if (k_off != nullptr) {
-      bh = blockIdx.x / nK;
-      const int j = blockIdx.x % nK;
+    const unsigned count = static_cast<unsigned>(BH) * (k_off != nullptr ? nK : 1);
+    const unsigned i = mean_warps == 8 ? blockIdx.x : blockIdx.x * 8 + threadIdx.x / 32;
+    int bh = i, start = 0, n = i < count ? N : 0;
+    if (k_off != nullptr && i < count) {
+      bh = i / nK;
+      const int j = i % nK;
       const int32_t* off = k_off + static_cast<size_t>(bh) * (nK + 1);
       start = off[j];
       n = cluster_rows(off, j, N);
-      if (n == 0) return;
     }
-    mean_key<D>(K, static_cast<long long>(bh) * N + start, n, means + static_cast<size_t>(blockIdx.x) * D);
+    mean_key<D>(K, static_cast<long long>(bh) * N + start, n, mean_warps, means + static_cast<size_t>(i) * D);
     return;
   }
   constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes, kUnroll = 2;
@@ -342,44 +358,63 @@ __device__ __forceinline__ void pack_units(const int32_t* off, const uint32_t* b
 constexpr int kPlanRun = 32;  // clusters that one warp packs; units do not cross runs (at most 31 units of a plane)
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr size_t kPlanSmem = 200 * 1024;  // the selection's bits both ways, if they fit
+// Up to this much of it two CTAs fit an SM, and those of the kept keys' means go beside the planning ones (1 x 4096 in 16 / 32
+// clusters: 66.8 us, 70.4 with a launch of their own).
+constexpr size_t kPlanBesideSmem = 96 * 1024;
 
-// The mean of the keys that a Q cluster keeps, from the means of the K clusters: d threads per Q cluster, one
-// per column.  0 for a cluster that keeps none.  list: kPlanThreads entries each of shared memory.
-__device__ void center_clusters(const int32_t* __restrict__ k_off, const int32_t* __restrict__ sel_count,
-                                const int32_t* __restrict__ sel_idx, int N, int nQ, int nK, int d, int rows, int first,
-                                const float* __restrict__ cluster_mean, float* __restrict__ center, int32_t* list,
-                                int32_t* list_rows) {
-  const int col = threadIdx.x % d, group = threadIdx.x / d;
-  const int row = first + group;  // plane * nQ + Q cluster
-  const int bh = row < rows ? row / nQ : 0;
-  const int cnt = row < rows ? min(max(sel_count[row], 0), nK) : 0;
-  const int32_t* off = k_off + static_cast<size_t>(bh) * (nK + 1);
-  const float* means = cluster_mean + static_cast<size_t>(bh) * nK * d + col;
-  float sum = 0.f, n = 0.f;
-  for (int e0 = 0; e0 < nK; e0 += d) {
-    const int e = e0 + col;
-    const int j = e < cnt ? sel_idx[static_cast<size_t>(row) * nK + e] : -1;
-    const int r = j >= 0 && j < nK ? cluster_rows(off, j, N) : 0;
-    list[threadIdx.x] = r > 0 ? j : 0;
-    list_rows[threadIdx.x] = r;
-    __syncthreads();
-    const int most = min(d, cnt - e0);
-#pragma unroll 8
-    for (int t = 0; t < most; ++t) {
-      const int w = list_rows[group * d + t];
-      const float m = w > 0 ? __ldg(means + static_cast<size_t>(list[group * d + t]) * d) : 0.f;
-      sum = fmaf(static_cast<float>(w), m, sum);
-      n += static_cast<float>(w);
+// The mean of the keys that a Q cluster keeps, from the means of the K clusters: a warp per Q cluster (row = plane nQ +
+// cluster), d / 32 columns per lane.  0 for a cluster that keeps none.
+template <class V, int P>  // V: the vector of P columns
+__device__ __forceinline__ void center_cluster(const int32_t* off, const int32_t* list, int cnt, int N, int nK,
+                                               const V* __restrict__ means, V* center) {
+  const int lane = threadIdx.x & 31;
+  float sum[P] = {}, n = 0.f;
+  for (int e0 = 0; e0 < cnt; e0 += 32) {
+    int j = e0 + lane < cnt ? list[e0 + lane] : -1;
+    const int rows = j >= 0 && j < nK ? cluster_rows(off, j, N) : 0;
+    if (rows == 0) j = -1;
+#pragma unroll 16
+    for (int t = 0; t < 32; ++t) {
+      const int k = __shfl_sync(0xffffffffu, j, t);
+      const float w = static_cast<float>(__shfl_sync(0xffffffffu, rows, t));
+      const V m = k >= 0 ? __ldg(means + static_cast<size_t>(k) * 32 + lane) : V{};
+#pragma unroll
+      for (int p = 0; p < P; ++p) sum[p] = fmaf(w, reinterpret_cast<const float*>(&m)[p], sum[p]);
+      n += w;
     }
-    __syncthreads();
   }
-  if (row < rows) {
-    const float c = n > 0.f ? sum / n : 0.f;
-    center[static_cast<size_t>(row) * d + col] = fabsf(c) < INFINITY ? c : 0.f;
+  V c;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    const float x = n > 0.f ? sum[p] / n : 0.f;
+    reinterpret_cast<float*>(&c)[p] = fabsf(x) < INFINITY ? x : 0.f;
   }
+  center[lane] = c;
 }
 
-// The first BH CTAs make the plans, the others the means of the kept keys.
+__device__ __forceinline__ void center_row(const int32_t* __restrict__ k_off, const int32_t* __restrict__ sel_count,
+                                           const int32_t* __restrict__ sel_idx, int N, int nQ, int nK, int d, int rows,
+                                           int row, const float* __restrict__ cluster_mean, float* __restrict__ center) {
+  if (row >= rows) return;
+  const int bh = row / nQ, cnt = min(max(sel_count[row], 0), nK);
+  const int32_t* off = k_off + static_cast<size_t>(bh) * (nK + 1);
+  const int32_t* list = sel_idx + static_cast<size_t>(row) * nK;
+  const float* means = cluster_mean + static_cast<size_t>(bh) * nK * d;
+  float* out = center + static_cast<size_t>(row) * d;
+  if (d == 128)
+    center_cluster<float4, 4>(off, list, cnt, N, nK, reinterpret_cast<const float4*>(means), reinterpret_cast<float4*>(out));
+  else
+    center_cluster<float2, 2>(off, list, cnt, N, nK, reinterpret_cast<const float2*>(means), reinterpret_cast<float2*>(out));
+}
+
+__global__ void __launch_bounds__(256)
+    bwd_center_kernel(const int32_t* __restrict__ k_off, const int32_t* __restrict__ sel_count,
+                      const int32_t* __restrict__ sel_idx, int N, int nQ, int nK, int d, int rows,
+                      const float* __restrict__ cluster_mean, float* __restrict__ center) {
+  center_row(k_off, sel_count, sel_idx, N, nQ, nK, d, rows, blockIdx.x * 8 + threadIdx.x / 32, cluster_mean, center);
+}
+
+// The first BH CTAs make the plans, others (if any) the means of the kept keys.
 __global__ void __launch_bounds__(kPlanThreads)
     bwd_plan_kernel(const int32_t* __restrict__ q_off, const int32_t* __restrict__ k_off,
                     const int32_t* __restrict__ sel_count, const int32_t* __restrict__ sel_idx, int N, int nQ, int nK,
@@ -390,9 +425,8 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int32_t k_offsets[kMaxClustersAssign + 1], q_offsets[kMaxClustersAssign + 1];
   __shared__ uint32_t k_rows[kPlanWarps], q_rows[kPlanWarps];  // the clusters that have rows
   if (static_cast<int>(blockIdx.x) >= BH) {
-    static_assert(kMaxClustersAssign >= kPlanThreads, "the offsets' arrays hold the lists");
-    center_clusters(k_off, sel_count, sel_idx, N, nQ, nK, d, BH * nQ, (blockIdx.x - BH) * (kPlanThreads / d), cluster_mean,
-                    center, k_offsets, q_offsets);
+    center_row(k_off, sel_count, sel_idx, N, nQ, nK, d, BH * nQ, (blockIdx.x - BH) * kPlanWarps + threadIdx.x / 32,
+               cluster_mean, center);
     return;
   }
   const int WQ = (nQ + 31) / 32, WK = (nK + 31) / 32;
@@ -485,13 +519,6 @@ struct BwdTmem {
   static constexpr uint32_t acc1 = 128;               // key unit: dV
   static constexpr uint32_t dp = 256, acc2 = 384;     // acc2: dK | dQ
 };
-
-// Which of the unit's clusters a row belongs to, by the offsets of its plane.
-__device__ __forceinline__ int row_segment(const int32_t* off, const BwdUnit un, int row) {
-  int seg = 0;
-  while (seg + 1 < un.nseg && off[un.cluster + seg + 1] <= un.row0 + row) ++seg;
-  return seg;
-}
 
 template <int D, bool DENSE, bool KV, int SPLIT, bool MULTI>
 __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, const BwdUnit un, const int bh,
@@ -947,7 +974,7 @@ __device__ __forceinline__ void bwd_unit(const BwdMaps& maps, const BwdArgs& a, 
       }
       uint4* dst = reinterpret_cast<uint4*>(out + (plane + (tk < 0 ? 0 : tk)) * D);
       size_t group = bh;  // whose center: the plane's, or the row's Q cluster's
-      if constexpr (!KV && !DENSE) group = static_cast<size_t>(bh) * a.nQ + un.cluster + row_segment(a.q_off + static_cast<size_t>(bh) * (a.nQ + 1), un, row);
+      if constexpr (!KV && !DENSE) group = static_cast<size_t>(bh) * a.nQ + un.cluster + bars->seg[row];
 #pragma unroll 1
       for (int c = c0; c < c0 + kChunks; ++c) {
         uint32_t v[32];
@@ -1101,8 +1128,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (warp < 4) {
       const int row = threadIdx.x;
       int seg = 0;  // this row's cluster among the unit's
-      if constexpr (!dense)
-        seg = row_segment(kv ? a.k_off + static_cast<size_t>(bh) * (a.nK + 1) : a.q_off + static_cast<size_t>(bh) * (a.nQ + 1), un, row);
+      if constexpr (!dense) {
+        const int32_t* off = kv ? a.k_off + static_cast<size_t>(bh) * (a.nK + 1) : a.q_off + static_cast<size_t>(bh) * (a.nQ + 1);
+        while (seg + 1 < un.nseg && off[un.cluster + seg + 1] <= un.row0 + row) ++seg;
+        bars->seg[row] = static_cast<uint8_t>(seg);
+      }
       uint32_t w[8] = {0x3f803f80u, 0x3f80u};
 #pragma unroll
       for (int k = 0; k < 6; ++k) w[2 + k] = seg == 2 * k ? 0x3f80u : (seg == 2 * k + 1 ? 0x3f800000u : 0u);
@@ -1161,12 +1191,13 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   const long long rows = static_cast<long long>(BH) * N;
   constexpr int kRows = 256 / (D / 8);  // rows per CTA pass
   const unsigned grid = static_cast<unsigned>(rows / kRows + 1 < 148 * 16 ? rows / kRows + 1 : 148 * 16);
-  bwd_prep_kernel<D><<<grid + static_cast<unsigned>(BH) * (dense ? 1 : nK), 256, 0, s>>>(static_cast<const uint4*>(in.O), static_cast<const uint4*>(in.dO),
+  const int mean_warps = dense || N >= kMeanWide * nK ? 8 : 1;
+  bwd_prep_kernel<D><<<grid + mean_ctas_of(BH, dense ? 1 : nK, mean_warps), 256, 0, s>>>(static_cast<const uint4*>(in.O), static_cast<const uint4*>(in.dO),
                                                in.lse, in.perm_q, static_cast<const uint4*>(in.K), N, rows,
                                                BH, sc.neg_lse2, sc.neg_delta,
                                                sc.lse_step, sc.delta_step, 1.f / scale,
                                                in.perm_q != nullptr ? static_cast<uint4*>(sc.dOp) : nullptr,
-                                               dense ? nullptr : in.k_off, nK, dense ? sc.center : sc.cluster_mean, st);
+                                               dense ? nullptr : in.k_off, nK, mean_warps, dense ? sc.center : sc.cluster_mean, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   BwdArgs a{};
@@ -1181,9 +1212,17 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
     const bool fits = k_bytes + nQ * row <= kPlanSmem;
     e = cudaFuncSetAttribute(bwd_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPlanSmem));
     if (e != cudaSuccess) return e;
-    constexpr int kCenters = kPlanThreads / D;  // Q clusters per CTA
-    const unsigned plan_grid = static_cast<unsigned>(BH + (static_cast<long long>(BH) * nQ + kCenters - 1) / kCenters);
-    bwd_plan_kernel<<<plan_grid, kPlanThreads, k_bytes + (fits ? nQ : kPlanWarps) * row, s>>>(
+    const size_t plan_smem = k_bytes + (fits ? nQ : kPlanWarps) * row;
+    const bool beside = plan_smem <= kPlanBesideSmem;
+    const int clusters = BH * nQ;
+    const unsigned plan_grid = static_cast<unsigned>(BH + (beside ? (clusters + kPlanWarps - 1) / kPlanWarps : 0));
+    if (!beside) {
+      bwd_center_kernel<<<static_cast<unsigned>((clusters + 7) / 8), 256, 0, s>>>(in.k_off, in.sel_count, in.sel_idx, N, nQ, nK, D,
+                                                                              clusters, sc.cluster_mean, sc.center);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    bwd_plan_kernel<<<plan_grid, kPlanThreads, plan_smem, s>>>(
         in.q_off, in.k_off, in.sel_count, in.sel_idx, N, nQ, nK, sc.keepers, sc.kept, fits, sc.k_units, a.k_per_head,
         sc.q_units, a.q_per_head, BH, D, sc.cluster_mean, sc.center, st);
     e = cudaGetLastError();

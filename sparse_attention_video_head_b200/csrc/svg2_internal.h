@@ -133,7 +133,8 @@ inline int attn_max_units_per_head(int N, int nQ) { return (N + 255) / 256 + nQ;
 inline int attn_unit_rows(int BH, int N) {
   return static_cast<long long>(BH) * ((N + 255) / 256) <= 74 ? 128 : 256;
 }
-// (at most this many per head; a plan too large for the one-launch plan kernel has more planes than that)
+// At most this many per head.  (A plan too large for the one-launch plan kernel is made of 256-row units whatever
+// attn_unit_rows says, and those are never more.)
 inline int attn_lse_units_per_head(int BH, int N, int nQ) {
   const int rows = attn_unit_rows(BH, N);
   return (N + rows - 1) / rows + nQ;

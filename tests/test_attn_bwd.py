@@ -585,8 +585,9 @@ def rel_norm(x, ref):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("N,nQ,d", [(5000, 100, 64), (5000, 5, 128), (1000, 20, 64), (400, 2, 128)])
-def test_large_keys_cost_nothing_to_rows_that_do_not_keep_them(N, nQ, d):
+@pytest.mark.parametrize("N,nQ,nK,d", [(5000, 100, 40, 64), (5000, 5, 40, 128), (1000, 20, 40, 64), (400, 2, 40, 128),
+                                        (3000, 900, 900, 128)])
+def test_large_keys_cost_nothing_to_rows_that_do_not_keep_them(N, nQ, nK, d):
     """K clusters 7 and 30 hold finite keys 300 past the others in every column; the odd Q clusters keep neither (30
     is kept by none), and the last rows of the plane, in no cluster, are larger still.  The dS that is handed over sums to
     some r_i, so what dQ subtracts has to come from the keys that the row keeps: the limit is the one of
@@ -595,7 +596,6 @@ def test_large_keys_cost_nothing_to_rows_that_do_not_keep_them(N, nQ, d):
     svg2 = require_gpu()
     g = gen(N + nQ)
     Q, K, V, dO = (randn(g, 1, 1, N, d) for _ in range(4))
-    nK = 40
     keep = torch.ones(nQ, nK, dtype=torch.bool)
     keep[:, 30] = False
     keep[1::2, 7] = False
