@@ -87,10 +87,10 @@ def gen_inputs(cfg, step=0, heads=None):
 
 
 # DRAM traffic of one sparse-attention launch from an ncu capture of a 4-head cut of the Wan-720p
-# layer (dram__bytes_read.sum + dram__bytes_write.sum = 241.2 MB + 62.4 MB), scaled by heads; valid
+# layer (dram__bytes_read.sum + dram__bytes_write.sum = 239.9 MB + 61.7 MB), scaled by heads; valid
 # only for the kernel source it was taken on (sha256 of svg2_attn.cu), else reported as null.
-ATTN_TRAFFIC = {"sha256": "813099e1cf16e259c9cfac4986f3db1f404937df60dc1d5301450e1c73866adf",
-                "workload": "wan720p", "heads_captured": 4, "bytes_captured": 241.22e6 + 62.42e6,
+ATTN_TRAFFIC = {"sha256": "7e32b772abe37fb6aa2a922bf96a1d892ace9ebe57501bedc84bcd68781487de",
+                "workload": "wan720p", "heads_captured": 4, "bytes_captured": 239.91e6 + 61.72e6,
                 "summary": "profiles/sparse_attn_kernel_wan720p_4heads.md"}
 
 
