@@ -28,6 +28,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "svg2_device.cuh"
 #include "svg2_internal.h"
 
@@ -150,42 +152,138 @@ static_assert(sizeof(BwdBars) <= kBarBytes, "shared memory");
 // the mean of up to kMeanRows evenly spaced K rows each, of a plane (dense) or of a K cluster.
 // ------------------------------------------------------------------------------------------------
 constexpr int kMeanRows = 512;
-// From this many rows per K cluster on a CTA takes a cluster's mean, below a warp does (gradients of 24 x 4096 x 128 in 1024
-// clusters: 1490 us with warps, 1537 with CTAs; 1 x 4096 x 64 in 32: 71.2 with warps, 66.8 with CTAs).
+// From this many rows per K cluster on a CTA takes a cluster's mean, below a warp does (plain means, gradients of 24 x 4096 x 128
+// in 1024 clusters: 1490 us with warps, 1537 with CTAs; 1 x 4096 x 64 in 32: 71.2 with warps, 66.8 with CTAs).
 constexpr int kMeanWide = 64;
 
-// W warps (all eight, or one each) per mean: of rows row0 .. row0 + n - 1 (n = 0: not written).
+// Keys far from the others that a row's softmax gives nothing must not move what its dQ subtracts either: with 10 % of
+// the keys 300 away and of no weight the plain mean put dQ off by 7e-2 of its norm.  So the values within one standard
+// deviation of the mean are averaged again, column by column (of two groups the smaller one lies past that), and where the
+// plain mean is further from theirs than twice their own standard deviation, theirs counts.
+struct MeanSums {  // of a column; first pass: sum, sum of squares, number; second: the same of x - mean, of those within reach
+  float a, b, n;
+};
+__device__ __forceinline__ float finite_or_0(float x) { return fabsf(x) < INFINITY ? x : 0.f; }
+__device__ __forceinline__ float first_mean(MeanSums s) { return s.n > 0.f ? finite_or_0(s.a / s.n) : 0.f; }
+__device__ __forceinline__ float mean_reach(MeanSums s, float mean) {
+  const float var = s.b / fmaxf(s.n, 1.f) - mean * mean;
+  return var < INFINITY ? sqrtf(fmaxf(var, 0.f)) : INFINITY;
+}
+// x with weight w; a NaN or infinity stays with the rows that keep its key
+__device__ __forceinline__ void add_within(MeanSums& s, float x, float mean, float reach, float w) {
+  x -= mean;
+  if (fabsf(x) <= reach && fabsf(x) < INFINITY) {
+    s.a = fmaf(w, x, s.a);
+    s.b = fmaf(w * x, x, s.b);
+    s.n += w;
+  }
+}
+__device__ __forceinline__ float settle_mean(float plain, float mean, MeanSums s) {
+  if (!(s.n > 0.f)) return plain;
+  const float off = s.a / s.n, d = plain - (mean + off);
+  return d * d > 4.f * (s.b / s.n - off * off) ? finite_or_0(mean + off) : plain;
+}
+
+// floor(t n / S) without a 64-bit division
+__device__ __forceinline__ int spaced_row(int t, int n, int S) {
+  return t * (n / S) + static_cast<int>(static_cast<unsigned>(t * (n % S)) / static_cast<unsigned>(S));
+}
+template <class F>
+__device__ __forceinline__ void each_value(uint4 w, F&& take) {  // take(column of eight, value)
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    take(2 * e, bf16lo_to_f32(u[e]));
+    take(2 * e + 1, bf16hi_to_f32(u[e]));
+  }
+}
+
+// The mean of up to kMeanRows evenly spaced rows of the n >= 1 from row0 on, by a CTA; kMeanSample of them stand for
+// all where the values within reach are looked for.
+constexpr int kMeanSample = 64;
+
 template <int D>
-__device__ void mean_key(const uint4* __restrict__ K, long long row0, int n, int W, float* __restrict__ mean) {
-  constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes, kGroups = 256 / kLanes;
+__device__ __forceinline__ void mean_wide(const uint4* __restrict__ K, long long row0, int n, float* __restrict__ mean) {
+  constexpr int kLanes = D / 8, kGroups = 256 / kLanes, kPicks = kMeanSample / kGroups;
+  constexpr int kPer = 256 / D;  // threads per column in the end
   __shared__ float part[kGroups][D];
-  const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes, groups = W * kPerWarp;
-  const int S = min(n, kMeanRows);
+  __shared__ uint4 sample[kMeanSample][kLanes];
+  const int sub = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int S = min(n, kMeanRows), each = (S + kGroups - 1) / kGroups;  // a group's rows follow one another
+  const int t0 = group * each, t1 = min(S, t0 + each);
+#pragma unroll
+  for (int k = 0; k < kPicks; ++k) {
+    const int i = k * each / kPicks, t = t0 + i;
+    const bool is = t < t1 && (k == 0 || i > (k - 1) * each / kPicks);
+    sample[k * kGroups + group][sub] = is ? __ldg(K + (row0 + spaced_row(t, n, S)) * kLanes + sub)
+                                          : make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);  // NaN: none
+  }
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 16
-  for (int t = group % groups; t < S; t += groups) {
-    // floor(t n / S) without a 64-bit division
-    const long long row = row0 + t * (n / S) + static_cast<int>(static_cast<unsigned>(t * (n % S)) / static_cast<unsigned>(S));
-    const uint4 w = __ldg(K + row * kLanes + sub);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = bf16lo_to_f32(u[e]), y = bf16hi_to_f32(u[e]);
-      acc[2 * e] += fabsf(x) < INFINITY ? x : 0.f;  // a NaN or infinity stays with the rows that keep its key
-      acc[2 * e + 1] += fabsf(y) < INFINITY ? y : 0.f;
-    }
-  }
+  for (int t = t0; t < t1; ++t)
+    each_value(__ldg(K + (row0 + spaced_row(t, n, S)) * kLanes + sub), [&](int e, float x) { acc[e] += finite_or_0(x); });
 #pragma unroll
   for (int e = 0; e < 8; ++e) part[group][sub * 8 + e] = acc[e];
   __syncthreads();
-  if (n == 0) return;
-  const int first = group / groups * groups;  // of the partial sums of this thread's mean
-  for (int c = threadIdx.x % (32 * W); c < D; c += 32 * W) {
-    float s = 0.f;
-    for (int g = 0; g < groups; ++g) s += part[first + g][c];
-    s /= static_cast<float>(S);
-    mean[c] = fabsf(s) < INFINITY ? s : 0.f;
+  const int col = threadIdx.x / kPer, h = threadIdx.x % kPer;  // a column's threads are neighbours
+  auto over_threads = [&](float v) {
+#pragma unroll
+    for (int o = 1; o < kPer; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  auto total = [&](MeanSums s) { return MeanSums{over_threads(s.a), over_threads(s.b), over_threads(s.n)}; };
+  float plain = 0.f, v[kMeanSample / kPer];
+#pragma unroll
+  for (int g = 0; g < kGroups / kPer; ++g) plain += part[g * kPer + h][col];
+  plain = finite_or_0(over_threads(plain) / static_cast<float>(S));
+  const __nv_bfloat16* values = reinterpret_cast<const __nv_bfloat16*>(sample);
+  MeanSums s{0.f, 0.f, 0.f};
+#pragma unroll
+  for (int r = 0; r < kMeanSample / kPer; ++r) {
+    v[r] = __bfloat162float(values[(r * kPer + h) * D + col]);
+    add_within(s, v[r], 0.f, INFINITY, 1.f);
   }
+  s = total(s);
+  const float m = first_mean(s), reach = mean_reach(s, m);
+  s = MeanSums{0.f, 0.f, 0.f};
+#pragma unroll
+  for (int r = 0; r < kMeanSample / kPer; ++r) add_within(s, v[r], m, reach, 1.f);
+  s = total(s);
+  if (h == 0) mean[col] = settle_mean(plain, m, s);
+}
+
+// The same by a warp, for few rows: all of the up to kMeanRows are looked at twice.
+template <int D>
+__device__ __forceinline__ void mean_warp(const uint4* __restrict__ K, long long row0, int n, float* __restrict__ mean) {
+  constexpr int kLanes = D / 8, kGroups = 32 / kLanes;
+  const int lane = threadIdx.x & 31, sub = lane % kLanes, S = min(n, kMeanRows);
+  MeanSums s[8];
+  float m[8], reach[8];
+  auto pass = [&](auto&& take) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] = MeanSums{0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int t = lane / kLanes; t < S; t += kGroups)
+      each_value(__ldg(K + (row0 + spaced_row(t, n, S)) * kLanes + sub), take);
+#pragma unroll
+    for (int o = kLanes; o < 32; o <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s[e].a += __shfl_xor_sync(0xffffffffu, s[e].a, o);
+        s[e].b += __shfl_xor_sync(0xffffffffu, s[e].b, o);
+        s[e].n += __shfl_xor_sync(0xffffffffu, s[e].n, o);
+      }
+  };
+  pass([&](int e, float x) { add_within(s[e], x, 0.f, INFINITY, 1.f); });
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    m[e] = first_mean(s[e]);
+    reach[e] = mean_reach(s[e], m[e]);
+  }
+  if (S > 2) pass([&](int e, float x) { add_within(s[e], x, m[e], reach[e], 1.f); });
+  if (lane < kLanes)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mean[sub * 8 + e] = S > 2 ? settle_mean(m[e], m[e], s[e]) : m[e];
 }
 
 // Rows of cluster i by its plane's offsets; malformed ones hold none.
@@ -194,35 +292,39 @@ __device__ __forceinline__ int cluster_rows(const int32_t* off, int i, int N) {
   return start < 0 || n <= 0 || start > N - n ? 0 : n;
 }
 
-__host__ __device__ __forceinline__ unsigned mean_ctas_of(int BH, int n, int mean_warps) {
+__host__ __device__ __forceinline__ unsigned mean_ctas_of(int BH, int n, bool wide) {
   const unsigned count = static_cast<unsigned>(BH) * n;
-  return mean_warps == 8 ? count : (count + 7) / 8;
+  return wide ? count : (count + 7) / 8;
 }
 
 template <int D>
-__global__ void __launch_bounds__(256) bwd_prep_kernel(const uint4* __restrict__ O, const uint4* __restrict__ dO,
+__global__ void __launch_bounds__(256, 4) bwd_prep_kernel(const uint4* __restrict__ O, const uint4* __restrict__ dO,
                                                        const float* __restrict__ lse, const int32_t* __restrict__ perm,
                                                        const uint4* __restrict__ K, int N, long long rows,
                                                        int BH, float* __restrict__ neg_lse2,
                                                        float* __restrict__ neg_delta, uint4* __restrict__ lse_step,
                                                        uint4* __restrict__ delta_step, float inv_scale,
                                                        uint4* __restrict__ dOp, const int32_t* __restrict__ k_off,
-                                                       int nK, int mean_warps, float* __restrict__ means,
+                                                       int nK, bool wide, float* __restrict__ means,
                                                        DeviceStatus* st) {
-  // means: of BH planes (k_off null), or of their nK clusters each, eight to a CTA where mean_warps is 1
-  const unsigned mean_ctas = mean_ctas_of(BH, k_off != nullptr ? nK : 1, mean_warps);
+  // means: of BH planes (k_off null), or of their nK clusters each, by a CTA or (wide false) by a warp
+  const unsigned mean_ctas = mean_ctas_of(BH, k_off != nullptr ? nK : 1, wide);
   if (blockIdx.x < mean_ctas) {
-    const unsigned count = static_cast<unsigned>(BH) * (k_off != nullptr ? nK : 1);
-    const unsigned i = mean_warps == 8 ? blockIdx.x : blockIdx.x * 8 + threadIdx.x / 32;
-    int bh = i, start = 0, n = i < count ? N : 0;
-    if (k_off != nullptr && i < count) {
+    const unsigned i = wide ? blockIdx.x : blockIdx.x * 8 + threadIdx.x / 32;
+    int bh = i, start = 0, n = N;
+    if (k_off != nullptr) {
+      if (i >= static_cast<unsigned>(BH) * nK) return;
       bh = i / nK;
       const int j = i % nK;
       const int32_t* off = k_off + static_cast<size_t>(bh) * (nK + 1);
       start = off[j];
       n = cluster_rows(off, j, N);
+      if (n == 0) return;  // (its mean is not read)
     }
-    mean_key<D>(K, static_cast<long long>(bh) * N + start, n, mean_warps, means + static_cast<size_t>(i) * D);
+    const long long row0 = static_cast<long long>(bh) * N + start;
+    float* mean = means + static_cast<size_t>(i) * D;
+    if (wide) mean_wide<D>(K, row0, n, mean);
+    else mean_warp<D>(K, row0, n, mean);
     return;
   }
   constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes, kUnroll = 2;
@@ -358,60 +460,94 @@ __device__ __forceinline__ void pack_units(const int32_t* off, const uint32_t* b
 constexpr int kPlanRun = 32;  // clusters that one warp packs; units do not cross runs (at most 31 units of a plane)
 constexpr int kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
 constexpr size_t kPlanSmem = 200 * 1024;  // the selection's bits both ways, if they fit
-// Up to this much of it two CTAs fit an SM, and those of the kept keys' means go beside the planning ones (1 x 4096 in 16 / 32
-// clusters: 66.8 us, 70.4 with a launch of their own).
+// Up to this much of it two CTAs fit an SM, and those of the kept keys' means go beside the planning ones, with four
+// warps per Q cluster (8 x 12480 in 64 / 256 clusters: both 33 us, 45 with two warps, 73 with one).  Otherwise they have a launch
+// of their own, a warp per Q cluster (24 x 4096 in 1024 / 1024: 165 us, 204 with four warps).
+constexpr int kCenterWarps = 4;
 constexpr size_t kPlanBesideSmem = 96 * 1024;
 
-// The mean of the keys that a Q cluster keeps, from the means of the K clusters: a warp per Q cluster (row = plane nQ +
-// cluster), d / 32 columns per lane.  0 for a cluster that keeps none.
-template <class V, int P>  // V: the vector of P columns
-__device__ __forceinline__ void center_cluster(const int32_t* off, const int32_t* list, int cnt, int N, int nK,
-                                               const V* __restrict__ means, V* center) {
-  const int lane = threadIdx.x & 31;
-  float sum[P] = {}, n = 0.f;
-  for (int e0 = 0; e0 < cnt; e0 += 32) {
-    int j = e0 + lane < cnt ? list[e0 + lane] : -1;
-    const int rows = j >= 0 && j < nK ? cluster_rows(off, j, N) : 0;
-    if (rows == 0) j = -1;
-#pragma unroll 16
-    for (int t = 0; t < 32; ++t) {
-      const int k = __shfl_sync(0xffffffffu, j, t);
-      const float w = static_cast<float>(__shfl_sync(0xffffffffu, rows, t));
-      const V m = k >= 0 ? __ldg(means + static_cast<size_t>(k) * 32 + lane) : V{};
+__device__ __forceinline__ void columns(float4 v, float (&x)[4]) { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
+__device__ __forceinline__ void columns(float2 v, float (&x)[2]) { x[0] = v.x, x[1] = v.y; }
+
+// The mean of the keys that a Q cluster keeps, from the means of the K clusters (settled as for the rows of one): W
+// warps per Q cluster, row = plane nQ + cluster, each with every W-th 32 of its list, d / 32 columns per lane.  0 for a
+// cluster that keeps none.  W > 1: all threads of a CTA call it; part: [warps][P][32 lanes].
+template <class V, int P, int W>  // V: the vector of P columns
+__device__ __forceinline__ void center_cluster(const int32_t* __restrict__ k_off, const int32_t* __restrict__ sel_count,
+                                               const int32_t* __restrict__ sel_idx, int N, int nQ, int nK, int rows,
+                                               int row, const float* __restrict__ cluster_mean,
+                                               float* __restrict__ center, MeanSums* part) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warp0 = warp / W * W;
+  const bool has = row < rows;
+  const int bh = has ? row / nQ : 0, cnt = has ? min(max(sel_count[row], 0), nK) : 0;
+  const int32_t* off = k_off + static_cast<size_t>(bh) * (nK + 1);
+  const int32_t* list = sel_idx + static_cast<size_t>(has ? row : 0) * nK;
+  const V* means = reinterpret_cast<const V*>(cluster_mean) + static_cast<size_t>(bh) * nK * 32 + lane;
+  MeanSums s[P];
+  auto pass = [&](auto&& take) {  // take(column, its cluster mean, the cluster's rows); s: the sums over all warps
 #pragma unroll
-      for (int p = 0; p < P; ++p) sum[p] = fmaf(w, reinterpret_cast<const float*>(&m)[p], sum[p]);
-      n += w;
+    for (int p = 0; p < P; ++p) s[p] = MeanSums{0.f, 0.f, 0.f};
+    for (int e0 = 32 * (warp - warp0); e0 < cnt; e0 += 32 * W) {
+      int j = e0 + lane < cnt ? list[e0 + lane] : -1;
+      const int n = j >= 0 && j < nK ? cluster_rows(off, j, N) : 0;
+      if (n == 0) j = -1;
+      for (int t0 = 0; t0 < min(32, cnt - e0); t0 += 8)
+#pragma unroll
+        for (int t = t0; t < t0 + 8; ++t) {
+          const int k = __shfl_sync(0xffffffffu, j, t);
+          const float w = static_cast<float>(__shfl_sync(0xffffffffu, n, t));
+          const V m = k >= 0 ? __ldg(means + static_cast<size_t>(k) * 32) : V{};
+          float x[P];
+          columns(m, x);
+#pragma unroll
+          for (int p = 0; p < P; ++p) take(p, x[p], w);
+        }
     }
-  }
-  V c;
+    if constexpr (W > 1) {
+      __syncthreads();  // (the sums of the pass before have been read)
+#pragma unroll
+      for (int p = 0; p < P; ++p) part[(warp * P + p) * 32 + lane] = s[p];
+      __syncthreads();
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        s[p] = MeanSums{0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const MeanSums o = part[((warp0 + w) * P + p) * 32 + lane];
+          s[p].a += o.a, s[p].b += o.b, s[p].n += o.n;
+        }
+      }
+    }
+  };
+  float mean[P], reach[P], c[P];
+  pass([&](int p, float x, float w) { add_within(s[p], x, 0.f, INFINITY, w); });
 #pragma unroll
   for (int p = 0; p < P; ++p) {
-    const float x = n > 0.f ? sum[p] / n : 0.f;
-    reinterpret_cast<float*>(&c)[p] = fabsf(x) < INFINITY ? x : 0.f;
+    mean[p] = first_mean(s[p]);
+    reach[p] = mean_reach(s[p], mean[p]);
   }
-  center[lane] = c;
+  pass([&](int p, float x, float w) { add_within(s[p], x, mean[p], reach[p], w); });
+  if (!has || warp != warp0) return;
+  V* out = reinterpret_cast<V*>(center) + static_cast<size_t>(row) * 32 + lane;
+#pragma unroll
+  for (int p = 0; p < P; ++p) c[p] = settle_mean(mean[p], mean[p], s[p]);
+  if constexpr (P == 4) *out = make_float4(c[0], c[1], c[2], c[3]);
+  else *out = make_float2(c[0], c[1]);
 }
 
-__device__ __forceinline__ void center_row(const int32_t* __restrict__ k_off, const int32_t* __restrict__ sel_count,
-                                           const int32_t* __restrict__ sel_idx, int N, int nQ, int nK, int d, int rows,
-                                           int row, const float* __restrict__ cluster_mean, float* __restrict__ center) {
-  if (row >= rows) return;
-  const int bh = row / nQ, cnt = min(max(sel_count[row], 0), nK);
-  const int32_t* off = k_off + static_cast<size_t>(bh) * (nK + 1);
-  const int32_t* list = sel_idx + static_cast<size_t>(row) * nK;
-  const float* means = cluster_mean + static_cast<size_t>(bh) * nK * d;
-  float* out = center + static_cast<size_t>(row) * d;
-  if (d == 128)
-    center_cluster<float4, 4>(off, list, cnt, N, nK, reinterpret_cast<const float4*>(means), reinterpret_cast<float4*>(out));
-  else
-    center_cluster<float2, 2>(off, list, cnt, N, nK, reinterpret_cast<const float2*>(means), reinterpret_cast<float2*>(out));
+template <int W>
+__device__ __forceinline__ void center_row(const int32_t* k_off, const int32_t* sel_count, const int32_t* sel_idx, int N,
+                                           int nQ, int nK, int d, int rows, int row, const float* cluster_mean, float* center,
+                                           MeanSums* part) {
+  if (d == 128) center_cluster<float4, 4, W>(k_off, sel_count, sel_idx, N, nQ, nK, rows, row, cluster_mean, center, part);
+  else center_cluster<float2, 2, W>(k_off, sel_count, sel_idx, N, nQ, nK, rows, row, cluster_mean, center, part);
 }
 
 __global__ void __launch_bounds__(256)
     bwd_center_kernel(const int32_t* __restrict__ k_off, const int32_t* __restrict__ sel_count,
                       const int32_t* __restrict__ sel_idx, int N, int nQ, int nK, int d, int rows,
                       const float* __restrict__ cluster_mean, float* __restrict__ center) {
-  center_row(k_off, sel_count, sel_idx, N, nQ, nK, d, rows, blockIdx.x * 8 + threadIdx.x / 32, cluster_mean, center);
+  center_row<1>(k_off, sel_count, sel_idx, N, nQ, nK, d, rows, blockIdx.x * 8 + threadIdx.x / 32, cluster_mean, center, nullptr);
 }
 
 // The first BH CTAs make the plans, others (if any) the means of the kept keys.
@@ -425,8 +561,9 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int32_t k_offsets[kMaxClustersAssign + 1], q_offsets[kMaxClustersAssign + 1];
   __shared__ uint32_t k_rows[kPlanWarps], q_rows[kPlanWarps];  // the clusters that have rows
   if (static_cast<int>(blockIdx.x) >= BH) {
-    center_row(k_off, sel_count, sel_idx, N, nQ, nK, d, BH * nQ, (blockIdx.x - BH) * kPlanWarps + threadIdx.x / 32,
-               cluster_mean, center);
+    center_row<kCenterWarps>(k_off, sel_count, sel_idx, N, nQ, nK, d, BH * nQ,
+                             (blockIdx.x - BH) * (kPlanWarps / kCenterWarps) + threadIdx.x / (32 * kCenterWarps), cluster_mean,
+                             center, reinterpret_cast<MeanSums*>(k_bits));
     return;
   }
   const int WQ = (nQ + 31) / 32, WK = (nK + 31) / 32;
@@ -1191,13 +1328,13 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
   const long long rows = static_cast<long long>(BH) * N;
   constexpr int kRows = 256 / (D / 8);  // rows per CTA pass
   const unsigned grid = static_cast<unsigned>(rows / kRows + 1 < 148 * 16 ? rows / kRows + 1 : 148 * 16);
-  const int mean_warps = dense || N >= kMeanWide * nK ? 8 : 1;
-  bwd_prep_kernel<D><<<grid + mean_ctas_of(BH, dense ? 1 : nK, mean_warps), 256, 0, s>>>(static_cast<const uint4*>(in.O), static_cast<const uint4*>(in.dO),
+  const bool wide = dense || N >= kMeanWide * nK;
+  bwd_prep_kernel<D><<<grid + mean_ctas_of(BH, dense ? 1 : nK, wide), 256, 0, s>>>(static_cast<const uint4*>(in.O), static_cast<const uint4*>(in.dO),
                                                in.lse, in.perm_q, static_cast<const uint4*>(in.K), N, rows,
                                                BH, sc.neg_lse2, sc.neg_delta,
                                                sc.lse_step, sc.delta_step, 1.f / scale,
                                                in.perm_q != nullptr ? static_cast<uint4*>(sc.dOp) : nullptr,
-                                               dense ? nullptr : in.k_off, nK, mean_warps, dense ? sc.center : sc.cluster_mean, st);
+                                               dense ? nullptr : in.k_off, nK, wide, dense ? sc.center : sc.cluster_mean, st);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   BwdArgs a{};
@@ -1212,17 +1349,18 @@ cudaError_t launch_bwd(const BwdInputs& in, int BH, int N, int nQ, int nK, float
     const bool fits = k_bytes + nQ * row <= kPlanSmem;
     e = cudaFuncSetAttribute(bwd_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPlanSmem));
     if (e != cudaSuccess) return e;
-    const size_t plan_smem = k_bytes + (fits ? nQ : kPlanWarps) * row;
-    const bool beside = plan_smem <= kPlanBesideSmem;
+    const size_t bits_smem = k_bytes + (fits ? nQ : kPlanWarps) * row;
+    const bool beside = bits_smem <= kPlanBesideSmem;
+    const size_t plan_smem = beside ? std::max(bits_smem, kPlanWarps * D * sizeof(MeanSums)) : bits_smem;
     const int clusters = BH * nQ;
-    const unsigned plan_grid = static_cast<unsigned>(BH + (beside ? (clusters + kPlanWarps - 1) / kPlanWarps : 0));
+    constexpr int kPerCta = kPlanWarps / kCenterWarps;
     if (!beside) {
       bwd_center_kernel<<<static_cast<unsigned>((clusters + 7) / 8), 256, 0, s>>>(in.k_off, in.sel_count, in.sel_idx, N, nQ, nK, D,
                                                                               clusters, sc.cluster_mean, sc.center);
       e = cudaGetLastError();
       if (e != cudaSuccess) return e;
     }
-    bwd_plan_kernel<<<plan_grid, kPlanThreads, plan_smem, s>>>(
+    bwd_plan_kernel<<<static_cast<unsigned>(BH + (beside ? (clusters + kPerCta - 1) / kPerCta : 0)), kPlanThreads, plan_smem, s>>>(
         in.q_off, in.k_off, in.sel_count, in.sel_idx, N, nQ, nK, sc.keepers, sc.kept, fits, sc.k_units, a.k_per_head,
         sc.q_units, a.q_per_head, BH, D, sc.cluster_mean, sc.center, st);
     e = cudaGetLastError();

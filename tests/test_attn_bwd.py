@@ -761,3 +761,31 @@ def test_sparse_wait_that_runs_out_is_reported_and_leaves_the_workspace_usable()
         assert svg2.svg2_check_status(ws)[0] == 5
         svg2.svg2_set_wait_budget(ws, 0)
         assert same(sparse_step(svg2, pl, Q, K, V, dO, 0.1, ws=ws), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,d", [(300, 64), (1000, 128), (4600, 64)])
+@pytest.mark.parametrize("part,far", [(0.02, 1e4), (0.04, 100.0), (0.1, 300.0), (0.2, 30.0)])
+def test_far_keys_of_no_weight_cost_dq_nothing(N, d, part, far):
+    """Some keys lie far from the others in every column, on the side that the queries turn away from: their P is 0, so
+    no product holds them, and what dQ subtracts must not either.  Dense with the far keys anywhere, and sparse with every
+    cluster kept, the far ones in clusters of their own and anywhere; also with what all keys have in common added.
+    The limit is 2 U."""
+    svg2 = require_gpu()
+    g = gen(N + d)
+    Q, K, V, dO = (randn(g, 1, 1, N, d) for _ in range(4))
+    Q = (Q.float() - 0.5).bfloat16()
+    away = torch.randperm(N, device="cuda", generator=g)
+    n = int(N * part)
+    for common in (0.0, 4.0):
+        x = K.float() + common
+        x[0, 0, away[:n]] += far
+        x = x.bfloat16()
+        ref, _ = formulas(Q[0, 0], x[0, 0], V[0, 0], dO[0, 0], d ** -0.5)
+        got = dense_step(svg2, Q, x, V, dO, d ** -0.5)
+        assert rel_norm(got["dQ"][0, 0], ref["dQ"]) <= 2 * U, (common, rel_norm(got["dQ"][0, 0], ref["dQ"]))
+        for nK in (3, 20):
+            pl = even_plan(0, 1, 1, N, 4, nK, torch.ones(4, nK, dtype=torch.bool))
+            for order in (away, torch.arange(N, device="cuda")):  # the far keys first, and where they are
+                got = sparse_step(svg2, pl, Q, x[:, :, order].contiguous(), V[:, :, order].contiguous(), dO, d ** -0.5, perms=False)
+                assert rel_norm(got["dQ"][0, 0], ref["dQ"]) <= 2 * U, (common, nK, rel_norm(got["dQ"][0, 0], ref["dQ"]))
