@@ -261,7 +261,8 @@ SVG2_API int svg2_sparse_attn_lse(const void* Qp, const void* Kp, const void* Vp
  *   dQ, dK, dV      bf16 [B,H,N,d], out, 16-byte aligned; they may alias neither each other nor an input.
  *   ws              at least svg2_dense_attn_bwd_workspace_size() bytes, 256-byte aligned (enough for
  *                   svg2_dense_attn_lse too); holds the status word.
- * P and dS are rounded to bf16 for the products, sums are float32; the results are the same on every run.
+ * P and dS are rounded to bf16 for the products, sums are float32; the results are the same on every run.  delta is taken from
+ * the bf16 O: where V's rows have a large mean in common, its rounding is what bounds dQ's accuracy on long rows.
  * A NaN in a row of Q, K, V, dO or lse reaches every gradient whose formula holds it, also where the forward left a
  * NaN key out; so does an infinity, but where its score is -inf, which is a P of 0.  Errors as svg2_dense_attn. */
 SVG2_API int svg2_dense_attn_bwd_workspace_size(int B, int H, int N, int d, size_t* bytes);

@@ -157,9 +157,10 @@ constexpr int kMeanRows = 512;
 constexpr int kMeanWide = 64;
 
 // Keys far from the others that a row's softmax gives nothing must not move what its dQ subtracts either: with 10 % of
-// the keys 300 away and of no weight the plain mean put dQ off by 7e-2 of its norm.  So the values within one standard
+// the keys 300 away and of no weight the plain mean put dQ off by 7e-2 of its norm, 2.4e-3 now.  So the values within one standard
 // deviation of the mean are averaged again, column by column (of two groups the smaller one lies past that), and where the
-// plain mean is further from theirs than twice their own standard deviation, theirs counts.
+// plain mean is further from theirs than twice their own standard deviation, theirs counts.  (Nothing here knows the weights: a
+// group that is taken for far and has weight costs its rows up to twice the error.)
 struct MeanSums {  // of a column; first pass: sum, sum of squares, number; second: the same of x - mean, of those within reach
   float a, b, n;
 };
